@@ -376,6 +376,46 @@ bool attn_aligned(int dtype, const void* Q, const void* K, const void* V, const 
              reinterpret_cast<uintptr_t>(O)) & 15u) == 0;
 }
 
+// Memory of the current device (or managed): a call for a cache of another
+// device must fail here, not on the GPU.
+bool is_here(const void* p) {
+    cudaPointerAttributes at;
+    int dev = 0;
+    if (!p || cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A cache's own description; the attention and the append only read it.
+bool valid_cache(const lsa_kv_cache* c) {
+    if (!c || c->batch < 1 || c->n_pages < 1 || c->ld_pages < 1 || c->hkv < 1 || !valid_d(c->d)) return false;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return false;
+    if (c->dtype != LSA_BF16 && c->dtype != LSA_E4M3) return false;
+    // page ids are int32; the last token of a row of the table stays within int32
+    if (c->n_pages > INT32_MAX || c->ld_pages > ((int64_t)1 << 31) / c->page || c->batch > 65535 || c->hkv > 4096)
+        return false;
+    if (!is_here(c->K) || !is_here(c->V) || !is_here(c->page_table)) return false;
+    if (!aligned16(c->K) || !aligned16(c->V)) return false;
+    return c->dtype != LSA_E4M3 || (is_here(c->K_scale) && is_here(c->V_scale));
+}
+
+// Rows up to new_tokens are indexed; the index's counts follow.
+int append_common(lsa_index* index, const void* K, const lsa_kv_cache* cache, int64_t n_new, void* stream) {
+    const lsa_build_params& p = index->p;
+    const int64_t new_tokens = index->n_tokens + n_new;
+    const int64_t first = index->nb;
+    const int64_t nb_new = new_tokens / p.pool;
+    int st = launch_append(index, K, cache, first, nb_new - first, as_stream(stream));
+    if (st != LSA_OK) return st;
+    index->n_tokens = new_tokens;
+    index->nb = nb_new;
+    return LSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -534,14 +574,52 @@ int lsa_append(lsa_index* index, const void* K, int64_t n_new, void* stream) {
     if (index->n_tokens + n_new > p.n_tokens + p.append_capacity) return LSA_ERR_INVALID_ARG;
     if (n_new == 0) return LSA_OK;
     if (!is_device_ptr(K)) return LSA_ERR_INVALID_ARG;
-    const int64_t new_tokens = index->n_tokens + n_new;
-    const int64_t first = index->nb;
-    const int64_t nb_new = new_tokens / p.pool;
-    int st = launch_append(index, K, first, nb_new - first, as_stream(stream));
-    if (st != LSA_OK) return st;
-    index->n_tokens = new_tokens;
-    index->nb = nb_new;
-    return LSA_OK;
+    return append_common(index, K, nullptr, n_new, stream);
+}
+
+int lsa_append_cached(lsa_index* index, const lsa_kv_cache* cache, int64_t n_new, void* stream) {
+    if (!live(index) || n_new < 0 || !valid_cache(cache)) return LSA_ERR_INVALID_ARG;
+    const lsa_build_params& p = index->p;
+    if (cache->batch != p.batch || cache->hkv != p.hkv || cache->d != p.d) return LSA_ERR_INVALID_ARG;
+    if (index->n_tokens + n_new > p.n_tokens + p.append_capacity) return LSA_ERR_INVALID_ARG;
+    if (n_new == 0) return LSA_OK;
+    return append_common(index, nullptr, cache, n_new, stream);
+}
+
+int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, const void* Q, int64_t n,
+                    const int64_t* cu, const int64_t* pos0, int32_t hq, int32_t dtype, const double* inv_freq,
+                    int32_t rot, int32_t interleaved, void* K_out, void* Q_out, void* stream) {
+    if (!valid_cache(cache)) return LSA_ERR_INVALID_ARG;
+    if (dtype != LSA_F32 && dtype != LSA_BF16) return LSA_ERR_INVALID_ARG;
+    if (rot < 0 || rot > cache->d || rot % 16 || (rot > 0 && !is_here(inv_freq))) return LSA_ERR_INVALID_ARG;
+    if (n < 0 || n > INT32_MAX || hq < 0 || hq > 65535 || !is_here(cu) || !is_here(pos0))
+        return LSA_ERR_INVALID_ARG;
+    if (n == 0) return LSA_OK;
+    if (!is_here(K) || !is_here(V) || !aligned16(K) || !aligned16(V)) return LSA_ERR_INVALID_ARG;
+    if (hq > 0 && (!is_here(Q) || !is_here(Q_out) || !aligned16(Q) || !aligned16(Q_out)))
+        return LSA_ERR_INVALID_ARG;
+    if (K_out && (!is_here(K_out) || !aligned16(K_out))) return LSA_ERR_INVALID_ARG;
+    int32_t* err = global_err_word();
+    if (!err) return LSA_ERR_CUDA;
+    return launch_cache_write(*cache, K, V, Q, n, cu, pos0, hq, dtype, inv_freq, rot, interleaved != 0, K_out, Q_out,
+                              err, as_stream(stream));
+}
+
+int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
+                   int32_t hq, int32_t dtype, int32_t max_sel, void* O, float* lse, void* stream) {
+    if (!valid_cache(cache)) return LSA_ERR_INVALID_ARG;
+    if (dtype != LSA_F32 && dtype != LSA_BF16) return LSA_ERR_INVALID_ARG;
+    if (nq < 0 || nq > INT32_MAX || hq < cache->hkv || hq % cache->hkv || hq / cache->hkv > 64 || max_sel < 1)
+        return LSA_ERR_INVALID_ARG;
+    if (nq == 0) return LSA_OK;
+    if (cache->batch * nq * hq > INT32_MAX / 16) return LSA_ERR_INVALID_ARG;
+    if (!is_here(Q) || !is_here(idx) || !is_here(cnt) || !is_here(O) || !aligned16(Q) ||
+        !aligned16(O))
+        return LSA_ERR_INVALID_ARG;
+    if (lse && !is_here(lse)) return LSA_ERR_INVALID_ARG;
+    int32_t* err = global_err_word();
+    if (!err) return LSA_ERR_CUDA;
+    return launch_cache_attn(*cache, Q, idx, cnt, nq, hq, dtype, max_sel, O, lse, err, as_stream(stream));
 }
 
 int lsa_relayout(lsa_index* index, void* stream) {

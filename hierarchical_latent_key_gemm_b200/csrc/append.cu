@@ -17,6 +17,7 @@
 // folds its best (distance, leaf) into one 64-bit key per block with
 // atomicMin, so ties go to the lower leaf); the ordered insertion, one CTA per
 // unit.
+#include "cache_common.cuh"
 #include "latent_common.cuh"
 
 namespace lsa {
@@ -47,9 +48,38 @@ struct AppArgs {
     int32_t* err;
 };
 
-// Latent of every new block: blockIdx.x = new block, blockIdx.y = unit.
+// Where the keys of the new blocks are: a dense buffer, or the pages of a cache.
 template <typename T>
-__global__ __launch_bounds__(kAppThreads) void append_latent_kernel(const T* __restrict__ K, const AppArgs a) {
+struct DenseKeys {
+    const T* K;
+    __device__ float mean(const AppArgs& a, int64_t bseq, int64_t b, int h, int k) const {
+        const T* p = K + ((bseq * a.ld_tokens + b * a.pool) * a.hkv + h) * a.d + k;
+        return mean_of_rows(p, (int64_t)a.hkv * a.d, a.pool);
+    }
+};
+template <typename CT>
+struct CachedKeys {
+    CacheArgs c;
+    __device__ float mean(const AppArgs& a, int64_t bseq, int64_t b, int h, int k) const {
+        return mean_of([&](int m) {
+            const int64_t tok = b * a.pool + m;
+            const int pid = cache_page(c, bseq, tok);
+            if (pid < 0) {
+                latch(a.err, kErrDevice);
+                return 0.f;
+            }
+            const CT* p = static_cast<const CT*>(c.K) + cache_row(c, pid, h, tok) * a.d + k;
+            if constexpr (sizeof(CT) == 1)
+                return e4m3x2_to_f32x2(*p).x * c.K_scale[(int64_t)pid * c.hkv + h];
+            else
+                return to_f32(*p);
+        }, a.pool);
+    }
+};
+
+// Latent of every new block: blockIdx.x = new block, blockIdx.y = unit.
+template <typename Keys>
+__global__ __launch_bounds__(kAppThreads) void append_latent_kernel(const Keys keys, const AppArgs a) {
     extern __shared__ float sm[];
     float* Ws = sm;                     // [d][r]
     float* mean = Ws + a.d * a.r;       // [d]
@@ -58,10 +88,7 @@ __global__ __launch_bounds__(kAppThreads) void append_latent_kernel(const T* __r
     const int64_t bseq = u / a.hkv;
     const int h = u % a.hkv;
     for (int e = threadIdx.x; e < a.d * a.r; e += kAppThreads) Ws[e] = a.W[e];
-    for (int k = threadIdx.x; k < a.d; k += kAppThreads) {
-        const T* p = K + ((bseq * a.ld_tokens + b * a.pool) * a.hkv + h) * a.d + k;
-        mean[k] = mean_of_rows(p, (int64_t)a.hkv * a.d, a.pool);
-    }
+    for (int k = threadIdx.x; k < a.d; k += kAppThreads) mean[k] = keys.mean(a, bseq, b, h, k);
     __syncthreads();
     for (int o = threadIdx.x; o < a.r; o += kAppThreads)
         a.Kl[((int64_t)u * a.nb_cap + b) * a.r + o] = latent_dot(mean, Ws, a.d, a.r, o);
@@ -180,9 +207,21 @@ __global__ __launch_bounds__(kAppThreads) void append_insert_kernel(const AppArg
     }
 }
 
+template <typename Keys>
+int launch_latent(const Keys& keys, const AppArgs& a, int64_t units, cudaStream_t s) {
+    const size_t smem = (size_t)(a.d * a.r + a.d) * sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(append_latent_kernel<Keys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return cuda_status(e);
+    note_launch();
+    append_latent_kernel<Keys><<<dim3((unsigned)a.n_new, (unsigned)units), kAppThreads, smem, s>>>(keys, a);
+    return LSA_OK;
+}
+
 }  // namespace
 
-int launch_append(lsa_index* ix, const void* K, int64_t first_block, int64_t n_new_blocks, cudaStream_t s) {
+int launch_append(lsa_index* ix, const void* K, const lsa_kv_cache* cache, int64_t first_block, int64_t n_new_blocks,
+                  cudaStream_t s) {
     if (n_new_blocks <= 0) return LSA_OK;
     const lsa_build_params& p = ix->p;
     AppArgs a{};
@@ -215,7 +254,6 @@ int launch_append(lsa_index* ix, const void* K, int64_t first_block, int64_t n_n
     a.first_block = first_block;
     a.n_new = n_new_blocks;
     a.err = ix->err;
-    const size_t smem_lat = (size_t)(p.d * p.r + p.d) * sizeof(float);
     const size_t smem_near = (size_t)n_new_blocks * p.r * sizeof(float);
     if (smem_near > 200 * 1024) return LSA_ERR_INVALID_ARG;
     Arena scratch;
@@ -224,29 +262,22 @@ int launch_append(lsa_index* ix, const void* K, int64_t first_block, int64_t n_n
     a.best = scratch.alloc<unsigned long long>(ix->units * n_new_blocks);
     if (scratch.status != LSA_OK) return scratch.status;
     cudaMemsetAsync(a.best, 0xff, ix->units * n_new_blocks * sizeof(unsigned long long), s);
-    cudaError_t e;
-    dim3 glat((unsigned)n_new_blocks, (unsigned)ix->units);
-    if (p.dtype == LSA_F32) {
-        e = cudaFuncSetAttribute(append_latent_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_lat);
-        if (e != cudaSuccess) return cuda_status(e);
-        note_launch();
-        append_latent_kernel<float><<<glat, kAppThreads, smem_lat, s>>>((const float*)K, a);
-    } else {
-        e = cudaFuncSetAttribute(append_latent_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_lat);
-        if (e != cudaSuccess) return cuda_status(e);
-        note_launch();
-        append_latent_kernel<__nv_bfloat16><<<glat, kAppThreads, smem_lat, s>>>((const __nv_bfloat16*)K, a);
-    }
-    e = cudaFuncSetAttribute(append_nearest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_near);
+    int st;
+    if (!K)
+        st = cache->dtype == LSA_E4M3 ? launch_latent(CachedKeys<uint8_t>{cache_args(*cache)}, a, ix->units, s)
+                                      : launch_latent(CachedKeys<__nv_bfloat16>{cache_args(*cache)}, a, ix->units, s);
+    else
+        st = p.dtype == LSA_F32 ? launch_latent(DenseKeys<float>{(const float*)K}, a, ix->units, s)
+                                : launch_latent(DenseKeys<__nv_bfloat16>{(const __nv_bfloat16*)K}, a, ix->units, s);
+    if (st != LSA_OK) return st;
+    cudaError_t e = cudaFuncSetAttribute(append_nearest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_near);
     if (e != cudaSuccess) return cuda_status(e);
     dim3 gnear((unsigned)((ix->L + kLeavesPerCta - 1) / kLeavesPerCta), (unsigned)ix->units);
     note_launch();
     append_nearest_kernel<<<gnear, kAppThreads, smem_near, s>>>(a);
     note_launch();
     append_insert_kernel<<<(unsigned)ix->units, kAppThreads, 0, s>>>(a);
-    const int st = cuda_status(cudaGetLastError());
+    st = cuda_status(cudaGetLastError());
     scratch.release();
     return st;
 }

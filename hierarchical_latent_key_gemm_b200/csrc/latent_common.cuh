@@ -9,13 +9,19 @@ namespace lsa {
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Mean of M values spaced `stride` elements apart: summed in order, then one
-// IEEE division.
+// Mean of M values given by at(0) .. at(M-1): summed in order, then one IEEE
+// division.
+template <typename F>
+__device__ __forceinline__ float mean_of(const F& at, int M) {
+    float s = 0.f;
+    for (int m = 0; m < M; ++m) s = __fadd_rn(s, at(m));
+    return __fdiv_rn(s, (float)M);
+}
+
+// Mean of M values spaced `stride` elements apart.
 template <typename T>
 __device__ __forceinline__ float mean_of_rows(const T* p, int64_t stride, int M) {
-    float s = 0.f;
-    for (int m = 0; m < M; ++m) s = __fadd_rn(s, to_f32(p[(int64_t)m * stride]));
-    return __fdiv_rn(s, (float)M);
+    return mean_of([&](int m) { return to_f32(p[(int64_t)m * stride]); }, M);
 }
 
 // Output o of mean (length d) times W [d][r]: one fma chain over inputs in order.

@@ -252,8 +252,16 @@ int launch_band_tc(const void* Q, const void* K, const void* V, int64_t batch, i
                    int32_t* err, cudaStream_t s);
 
 // ---------------------------------------------------------------- append
-int launch_append(lsa_index* ix, const void* K, int64_t first_block, int64_t n_new_blocks,
+// K: dense keys, or null and the keys come from the cache's pages.
+int launch_append(lsa_index* ix, const void* K, const lsa_kv_cache* cache, int64_t first_block, int64_t n_new_blocks,
                   cudaStream_t s);
+
+// ---------------------------------------------------------------- paged cache
+int launch_cache_write(const lsa_kv_cache& cache, const void* K, const void* V, const void* Q, int64_t n,
+                       const int64_t* cu, const int64_t* pos0, int hq, int dtype, const double* inv_freq, int rot,
+                       int interleaved, void* K_out, void* Q_out, int32_t* err, cudaStream_t s);
+int launch_cache_attn(const lsa_kv_cache& cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
+                      int hq, int dtype, int max_sel, void* O, float* lse, int32_t* err, cudaStream_t s);
 
 // ---------------------------------------------------------------- tree finish
 // Given leaf labels with their stable order, the upper-level parents with

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_PKG, "liblsa.so")
 
 LSA_OK, LSA_ERR_INVALID_ARG, LSA_ERR_CUDA, LSA_ERR_OOM = 0, 1, 2, 3
 LSA_ERR_INEXACT, LSA_ERR_TIMEOUT, LSA_ERR_DEVICE, LSA_ERR_CAPACITY = 4, 5, 6, 7
-LSA_F32, LSA_BF16 = 0, 1
+LSA_F32, LSA_BF16, LSA_E4M3 = 0, 1, 2
 LSA_MAX_LEVELS = 4
 (LSA_GET_CENTROIDS, LSA_GET_PARENT, LSA_GET_LEAF_OF_BLOCK, LSA_GET_MINPOS,
  LSA_GET_OBJECTIVE, LSA_GET_LATENT, LSA_GET_LEAF_COUNT) = range(7)
@@ -50,6 +50,12 @@ class IndexInfo(C.Structure):
                 ("sink", C.c_int32), ("grid_log2", C.c_int32)]
 
 
+class KVCacheDesc(C.Structure):
+    _fields_ = [("n_pages", C.c_int64), ("batch", C.c_int64), ("ld_pages", C.c_int64), ("page", C.c_int32),
+                ("hkv", C.c_int32), ("d", C.c_int32), ("dtype", C.c_int32), ("K", C.c_void_p), ("V", C.c_void_p),
+                ("K_scale", C.c_void_p), ("V_scale", C.c_void_p), ("page_table", C.c_void_p)]
+
+
 _vp, _i64, _i32 = C.c_void_p, C.c_int64, C.c_int32
 _SIGS = {
     "lsa_build_index": (_i32, [C.POINTER(BuildParams), _vp, _vp, _vp, C.POINTER(_vp)]),
@@ -64,6 +70,10 @@ _SIGS = {
     "lsa_sparse_attn_banded": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32,
                                       _i64, _i32, _i32, _vp, _vp, _vp]),
     "lsa_append": (_i32, [_vp, _vp, _i64, _vp]),
+    "lsa_append_cached": (_i32, [_vp, C.POINTER(KVCacheDesc), _i64, _vp]),
+    "lsa_cache_write": (_i32, [C.POINTER(KVCacheDesc), _vp, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _vp, _i32, _i32,
+                               _vp, _vp, _vp]),
+    "lsa_cache_attn": (_i32, [C.POINTER(KVCacheDesc), _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]),
     "lsa_relayout": (_i32, [_vp, _vp]),
     "lsa_refresh_centroids": (_i32, [_vp, _vp]),
     "lsa_pca_map": (_i32, [_vp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
@@ -536,6 +546,148 @@ def lsa_merge_attn(O_parts, lse_parts, O=None, lse=None, want_lse=True, stream=N
                              int(hq), int(d), dtype_code(O), _ptr(O), _typed(lse, torch.float32, "lse"),
                              _stream(stream)), "lsa_merge_attn")
     return O, lse
+
+
+# ------------------------------------------------------------ paged KV cache
+class KVCache:
+    """A paged cache of keys and values (lsa_kv_cache) over the caller's
+    tensors: pools K, V [n_pages, hkv, page, d], bfloat16 or float8_e4m3fn, the
+    latter with scales [n_pages, hkv] float32 (value = code * scale), and
+    page_table [batch, ld_pages] int32: token t of sequence b is slot t % page
+    of page page_table[b, t // page].  The tensors are held, not copied: a
+    server updates page_table in place as it hands out pages."""
+
+    def __init__(self, K, V, page_table, K_scale=None, V_scale=None):
+        if K.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("K and V must be [n_pages, hkv, page, d] and page_table [batch, ld_pages]")
+        n_pages, hkv, page, d = K.shape
+        if K.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or V.dtype != K.dtype:
+            raise ValueError(f"K and V must both be bfloat16 or float8_e4m3fn, got {K.dtype} and {V.dtype}")
+        _shape(V, K.shape, "V")
+        self.scaled = K.dtype == torch.float8_e4m3fn
+        if self.scaled:
+            if K_scale is None or V_scale is None:
+                raise ValueError("float8 pages need K_scale and V_scale")
+            _shape(K_scale, (n_pages, hkv), "K_scale")
+            _shape(V_scale, (n_pages, hkv), "V_scale")
+        elif K_scale is not None or V_scale is not None:
+            raise ValueError("bfloat16 pages have no scales")
+        if page not in (16, 32, 64, 128) or d not in (64, 128):
+            raise ValueError(f"pages hold 16, 32, 64 or 128 tokens of 64 or 128 components, got {page} and {d}")
+        self.K, self.V, self.page_table, self.K_scale, self.V_scale = K, V, page_table, K_scale, V_scale
+        self.device = K.device
+        _on_device(self.device, V=V, page_table=page_table, K_scale=K_scale, V_scale=V_scale)
+        self.batch, self.hkv, self.page, self.d = page_table.shape[0], hkv, page, d
+        self.desc = KVCacheDesc(n_pages, self.batch, page_table.shape[1], page, hkv, d,
+                                LSA_E4M3 if self.scaled else LSA_BF16, _ptr(K), _ptr(V),
+                                _typed(K_scale, torch.float32, "K_scale"), _typed(V_scale, torch.float32, "V_scale"),
+                                _typed(page_table, torch.int32, "page_table"))
+
+
+def make_kv_cache(batch, max_tokens, hkv, d, page=64, dtype=torch.float8_e4m3fn, n_pages=None, device="cuda"):
+    """A KVCache with pools of its own.  Without n_pages every sequence gets
+    the pages of max_tokens tokens, handed out in order; with it the pool has
+    that many pages and the table starts out empty (-1) for the caller to fill."""
+    per = -(-int(max_tokens) // page)
+    if n_pages is None:
+        n_pages = batch * per
+        table = torch.arange(n_pages, dtype=torch.int32, device=device).view(batch, per)
+    else:
+        table = torch.full((batch, per), -1, dtype=torch.int32, device=device)
+    pools = [torch.zeros((n_pages, hkv, page, d), dtype=dtype, device=device) for _ in range(2)]
+    scales = [None, None]
+    if dtype == torch.float8_e4m3fn:
+        scales = [torch.ones((n_pages, hkv), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(pools[0], pools[1], table, scales[0], scales[1])
+
+
+def _on_device(device, **ts):
+    for name, t in ts.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+
+
+def lsa_cache_write(cache: KVCache, K, V, cu, pos0, Q=None, inv_freq=None, interleaved=False, K_out=None, Q_out=None,
+                    want_K=False, stream=None):
+    """New tokens into the cache's pages, keys (and the queries Q) rotated on
+    the way.  K, V [n, hkv, d] and Q [n, hq, d], float32 or bfloat16; rows
+    cu[b] .. cu[b+1]-1 are sequence b's, from position pos0[b] on (cu [batch+1]
+    and pos0 [batch], int64); inv_freq [rot/2] float64 or None (no rotation).
+    Returns (Q_out, K_out): the rotated queries (None without Q) and, when
+    K_out is given or want_K is set, the rotated keys.  K_out may be K, Q_out
+    may be Q."""
+    if K.dim() != 3:
+        raise ValueError(f"K must be [n, hkv, d], got shape {tuple(K.shape)}")
+    n, hq = K.shape[0], 0
+    _shape(K, (n, cache.hkv, cache.d), "K")
+    _shape(V, K.shape, "V")
+    _shape(cu, (cache.batch + 1,), "cu")
+    _shape(pos0, (cache.batch,), "pos0")
+    if Q is not None:
+        if Q.dim() != 3:
+            raise ValueError(f"Q must be [n, hq, d], got shape {tuple(Q.shape)}")
+        hq = Q.shape[1]
+        _shape(Q, (n, hq, cache.d), "Q")
+        if Q_out is None:
+            Q_out = torch.empty_like(Q)
+        _shape(Q_out, Q.shape, "Q_out")
+    elif Q_out is not None:
+        raise ValueError("Q_out without Q")
+    if K_out is None and want_K:
+        K_out = torch.empty_like(K)
+    _shape(K_out, K.shape, "K_out")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError(f"inv_freq must be [rot/2], got shape {tuple(inv_freq.shape)}")
+        rot = 2 * inv_freq.shape[0]
+        if rot % 16 or rot > cache.d:
+            raise ValueError(f"the rotated components must be a multiple of 16 up to {cache.d}, got {rot}")
+    _same_dtype(K, V, Q, K_out, Q_out)
+    _on_device(cache.device, K=K, V=V, Q=Q, cu=cu, pos0=pos0, inv_freq=inv_freq, K_out=K_out, Q_out=Q_out)
+    st = lib().lsa_cache_write(C.byref(cache.desc), _ptr(K), _ptr(V), _ptr(Q), n, _typed(cu, torch.int64, "cu"),
+                               _typed(pos0, torch.int64, "pos0"), hq, dtype_code(K),
+                               _typed(inv_freq, torch.float64, "inv_freq"), rot, int(bool(interleaved)), _ptr(K_out),
+                               _ptr(Q_out), _stream(stream))
+    _ok(st, "lsa_cache_write")
+    return Q_out, K_out
+
+
+def lsa_cache_attn(cache: KVCache, Q, idx, cnt, O=None, lse=None, want_lse=True, stream=None):
+    """lsa_sparse_attn with the selected rows read from the cache: Q [batch,
+    nq, hq, d] float32 or bfloat16, idx [batch, nq, hkv, max_sel], cnt [batch,
+    nq, hkv]; returns (O, lse)."""
+    if Q.dim() != 4:
+        raise ValueError(f"Q must be [batch, nq, hq, d], got shape {tuple(Q.shape)}")
+    B, nq, hq, d = Q.shape
+    _shape(Q, (cache.batch, nq, hq, cache.d), "Q")
+    if idx.dim() != 4:
+        raise ValueError(f"idx must be [batch, nq, hkv, max_sel], got shape {tuple(idx.shape)}")
+    max_sel = idx.shape[3]
+    _shape(idx, (B, nq, cache.hkv, max_sel), "idx")
+    _shape(cnt, (B, nq, cache.hkv), "cnt")
+    if O is None:
+        O = torch.empty_like(Q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, nq, hq), dtype=torch.float32, device=Q.device)
+    _shape(O, Q.shape, "O")
+    _shape(lse, (B, nq, hq), "lse")
+    _same_dtype(Q, O)
+    _on_device(cache.device, Q=Q, idx=idx, cnt=cnt, O=O, lse=lse)
+    st = lib().lsa_cache_attn(C.byref(cache.desc), _ptr(Q), _typed(idx, torch.int32, "idx"),
+                              _typed(cnt, torch.int32, "cnt"), nq, hq, dtype_code(Q), max_sel, _ptr(O),
+                              _typed(lse, torch.float32, "lse"), _stream(stream))
+    _ok(st, "lsa_cache_attn")
+    return O, lse
+
+
+def lsa_append_cached(index: Index, cache: KVCache, n_new: int, stream=None):
+    """lsa_append with the new tokens' keys read from the cache's pages."""
+    p = index.params
+    if (cache.batch, cache.hkv, cache.d) != (p.batch, p.hkv, p.d):
+        raise ValueError(f"the cache holds (batch, hkv, d) = {(cache.batch, cache.hkv, cache.d)}, the index "
+                         f"{(p.batch, p.hkv, p.d)}")
+    _ok(lib().lsa_append_cached(index.handle, C.byref(cache.desc), int(n_new), _stream(stream)), "lsa_append_cached")
 
 
 def _host_ptr(t, dtype, shape, name):

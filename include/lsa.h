@@ -58,7 +58,11 @@ typedef enum {
     LSA_ERR_CAPACITY = 7       /* lsa_append found a leaf with no free slot */
 } lsa_status;
 
-typedef enum { LSA_F32 = 0, LSA_BF16 = 1 } lsa_dtype;
+typedef enum {
+    LSA_F32 = 0,
+    LSA_BF16 = 1,
+    LSA_E4M3 = 2               /* 8-bit float (4 exponent, 3 mantissa bits, no infinities): lsa_kv_cache pages only */
+} lsa_dtype;
 
 #define LSA_MAX_LEVELS 4
 
@@ -393,6 +397,90 @@ int lsa_relayout(lsa_index* index, void* stream);
  *    dead handle; a broken grid precondition latches LSA_ERR_INEXACT.
  * [p5 step 1: keys clustered into buckets organised as a hierarchy] */
 int lsa_refresh_centroids(lsa_index* index, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Paged KV cache.  The pages say only that keys and values of millions of
+ * tokens have to stay resident while a response is generated ([p1]; [p4]
+ * "Prompt processing is not response generation"); this is the layout a server
+ * of many sequences keeps them in: fixed pages handed out as sequences grow,
+ * in bf16 or in 8 bits with a scale for each page and head.  The selection
+ * (lsa_select) is unchanged; lsa_cache_write fills the pages, lsa_cache_attn
+ * attends selection rows from them, lsa_append_cached keeps the index up from
+ * them. */
+typedef struct {
+    int64_t n_pages;           /* pages in the pools */
+    int64_t batch;             /* sequences (rows of page_table) */
+    int64_t ld_pages;          /* entries per page_table row */
+    int32_t page;              /* tokens per page: 16, 32, 64 or 128 */
+    int32_t hkv;               /* KV heads */
+    int32_t d;                 /* head dimension: 64 or 128 */
+    int32_t dtype;             /* LSA_BF16 or LSA_E4M3 */
+    void* K;                   /* device [n_pages][hkv][page][d], 16-byte aligned */
+    void* V;                   /* device [n_pages][hkv][page][d], 16-byte aligned */
+    float* K_scale;            /* device [n_pages][hkv] (LSA_E4M3; ignored for LSA_BF16): */
+    float* V_scale;            /*   value = code * scale, 2^-64 <= scale <= 2^64 */
+    const int32_t* page_table; /* device [batch][ld_pages]: token t of sequence b is slot t % page of page
+                                  page_table[b][t / page]; entries of pages not yet given out are not read */
+} lsa_kv_cache;
+
+/* Write new tokens' keys and values into the cache, with the position rotation
+ * applied to the keys (and to the step's queries) on the way.
+ *  K, V: device [n][hkv][d], Q: device [n][hq][d], all of dtype (LSA_F32 or
+ *      LSA_BF16); Q may be NULL with hq = 0.  V is not rotated.
+ *  cu: device int64 [batch+1], ascending: rows cu[b] .. cu[b+1]-1 are the new
+ *      tokens of sequence b, at positions pos0[b], pos0[b]+1, ... (device int64
+ *      [batch]); pos0[b] tokens are in its pages already.  A sequence may bring
+ *      no token; rows outside [cu[0], cu[batch]) (padding) are not read and
+ *      their outputs not written.
+ *  inv_freq: device double [rot/2] or NULL with rot = 0.  Pair i of a token at
+ *      position t is turned by t * inv_freq[i]: (x, y) -> (x cos - y sin,
+ *      x sin + y cos).  rot: a multiple of 16, 0 <= rot <= d; pair i is
+ *      components (i, i + rot/2), or (2i, 2i+1) when interleaved != 0;
+ *      components from rot on are not turned.  The angle is formed in fp64, so
+ *      positions of many millions keep their phase.
+ *  K_out [n][hkv][d], Q_out [n][hq][d]: device, of dtype, the rotated keys and
+ *      queries, or NULL; K_out may be K and Q_out may be Q.  hq > 0 needs Q_out.
+ * LSA_E4M3 pages: one power-of-two scale per (page, head), for K and for V:
+ * the smallest 2^e, -64 <= e <= 64, with |x| <= lim 2^e over the finite
+ * elements the call writes there; lim = 448 for V and, before the rotation, 316
+ * for K (a rotation grows a component by at most sqrt(2)).  A page that already
+ * holds tokens of the sequence keeps the larger of that and its scale, and what
+ * it holds is rounded to the larger scale; a page written from its first slot
+ * on starts afresh.  Codes are rounded to nearest even; values too large for
+ * the largest scale saturate; a value that is NaN or infinite is stored as NaN.
+ * LSA_BF16 pages hold the rounded values.  Slots behind the last token keep
+ * what they held.
+ *  - The pages that one call writes must be distinct (no two sequences append
+ *    into one page).
+ *  - Found on the device and latched as LSA_ERR_DEVICE: cu not ascending within
+ *    [0, n] (nothing is written); a negative position, a position past the page
+ *    table or a page id outside [0, n_pages) (that page's tokens are skipped).
+ *  - No allocation, one kernel, no state kept: capturable. */
+int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, const void* Q, int64_t n,
+                    const int64_t* cu, const int64_t* pos0, int32_t hq, int32_t dtype, const double* inv_freq,
+                    int32_t rot, int32_t interleaved, void* K_out, void* Q_out, void* stream);
+
+/* lsa_sparse_attn with the rows read from the cache: the same softmax over the
+ * selected tokens of each row, keys and values being the cache's values.
+ *  Q: device [batch][nq][hq][d] of dtype (LSA_F32 or LSA_BF16); idx, cnt as
+ *      lsa_select writes them (entries past cnt are ignored); hq / hkv <= 64.
+ *  O: device [batch][nq][hq][d] of dtype; lse: device float [batch][nq][hq] or
+ *      NULL.  Q, O 16-byte aligned.
+ * A row with cnt = 0 yields O = 0 and lse = -inf.  A token past the page table
+ * or on a page id outside [0, n_pages) is skipped and latched as
+ * LSA_ERR_DEVICE.  Only the selected tokens are read, so what stale or empty
+ * slots hold does not matter.  Sums, maxima and products are accumulated in
+ * fp32; the same inputs give the same bits.  No allocation, one kernel:
+ * capturable. */
+int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
+                   int32_t hq, int32_t dtype, int32_t max_sel, void* O, float* lse, void* stream);
+
+/* lsa_append with the new tokens read from the cache's pages (lsa_cache_write
+ * has written them): the blocks they complete are pooled from the cache's
+ * values.  The cache's batch, hkv and d must be the index's.  A token past the
+ * page table or on a page id outside [0, n_pages) counts as zeros and latches
+ * LSA_ERR_DEVICE in the index.  Everything else as lsa_append. */
+int lsa_append_cached(lsa_index* index, const lsa_kv_cache* cache, int64_t n_new, void* stream);
 
 /* Stage calls, exposed for checks and for callers that compose the path. */
 

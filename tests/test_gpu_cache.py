@@ -1,0 +1,647 @@
+"""Paged KV cache on the GPU: the write with rotation and 8-bit rounding, the
+attention over selected rows of the cache and the index upkeep from its pages,
+against plain float64 statements of the same."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from hierarchical_latent_key_gemm_b200 import lsa
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+HALF_STEP = {BF: 2.0 ** -8, F32: 2.0 ** -24}     # a rounding's largest relative error
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    assert lsa.lsa_check() == lsa.LSA_OK
+    yield
+    torch.cuda.synchronize()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _values(cache, which):
+    """The pool's values [n_pages, hkv, page, d] in float64 numpy."""
+    pool, scale = getattr(cache, which), getattr(cache, which + "_scale")
+    x = pool.double()
+    return (x if scale is None else x * scale.double()[:, :, None, None]).cpu().numpy()
+
+
+def _shuffled_cache(batch, tokens, hkv, d, page, dtype, seed, spare=2):
+    """A cache whose pages are handed out in random order, garbage (NaN too) in every slot."""
+    g = _gen(seed)
+    per = -(-tokens // page)
+    c = lsa.make_kv_cache(batch, per * page, hkv, d, page, dtype, n_pages=batch * per + spare)
+    c.page_table.copy_(torch.randperm(batch * per + spare, generator=g, device="cuda")[:batch * per].view(batch, per))
+    raw = torch.randint(0, 256, c.K.shape + (c.K.element_size(),), generator=g, device="cuda").to(torch.uint8)
+    c.K.view(torch.uint8).copy_(raw.view(c.K.view(torch.uint8).shape))
+    c.V.view(torch.uint8).copy_(raw.flip(0).view(c.K.view(torch.uint8).shape))
+    return c
+
+
+def _inv_freq(rot, base=10000.0):
+    return base ** (-torch.arange(rot // 2, dtype=torch.float64, device="cuda") / max(1, rot // 2)) if rot else None
+
+
+def _new_tokens(lens, hkv, hq, d, io, seed, pad=0, loud=()):
+    g = _gen(seed)
+    n = sum(lens) + pad
+    mk = lambda h: (torch.randn(n, h, d, generator=g, device="cuda")
+                    * torch.exp(0.5 * torch.randn(h, d, generator=g, device="cuda"))).to(io)
+    K, V, Q = mk(hkv), mk(hkv), mk(hq) if hq else None
+    for t, f in loud:
+        K[t] *= f
+        V[t] *= f
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int64, device="cuda")
+    return K, V, Q, cu
+
+
+def _check_write(cache, before, K, V, Q, K_out, Q_out, cu, pos0, rot, interleaved):
+    """Everything a write leaves behind against the float64 statement of it."""
+    io, page = K.dtype, cache.page
+    f64 = lambda t: t.double().cpu().numpy()
+    f = np.zeros(0) if rot == 0 else _inv_freq(rot).cpu().numpy()
+    cu, pos0 = cu.tolist(), pos0.tolist()
+    pos = np.concatenate([pos0[b] + np.arange(cu[b + 1] - cu[b]) for b in range(cache.batch)])
+    n = cu[-1]
+    # a turned component: cos, sin and two products and a sum in fp32, each within 2^-23 of |x| + |y| <= 2 amax
+    slack = lambda x: 2.0 ** -21 * 2 * np.abs(x).max(-1, keepdims=True) if rot else 0.0
+    for raw, out in ((Q, Q_out), (K, K_out)):
+        if raw is None or out is None:
+            continue
+        x = f64(raw)[:n]
+        want = O.rotate(x, pos, f, interleaved)
+        assert np.all(np.abs(f64(out)[:n] - want) <= HALF_STEP[io] * np.abs(want) + slack(x))
+    k = O.rotate(f64(K)[:n], pos, f, interleaved)
+    v = f64(V)[:n]
+    table = cache.page_table.cpu().numpy()
+    touched = set()
+    for name, new, raw, lim in (("K", k, f64(K), O.LIM_K), ("V", v, f64(V), O.LIM_V)):
+        got, held = _values(cache, name), before[name]
+        sl = slack(f64(K)[:n]) if name == "K" and rot else np.zeros((n, cache.hkv, 1))
+        for b in range(cache.batch):
+            t = cu[b]
+            while t < cu[b + 1]:
+                p = pos0[b] + t - cu[b]
+                first, pid = p % page, int(table[b, p // page])
+                m = min(page - first, cu[b + 1] - t)
+                touched.add(pid)
+                for h in range(cache.hkv):
+                    if cache.scaled:
+                        s, want = O.write_page(held[pid, h], before[name + "_scale"][pid, h], first,
+                                               raw[t:t + m, h], new[t:t + m, h], lim)
+                        assert float(getattr(cache, name + "_scale")[pid, h]) == s
+                        assert np.array_equal(got[pid, h, :first], want[:first], equal_nan=True)
+                        w = want[first:first + m]
+                        g = got[pid, h, first:first + m]
+                        if name == "V":
+                            assert np.array_equal(g, O.round_e4m3(w / s) * s, equal_nan=True)
+                        else:
+                            ok = np.maximum(2.0 ** -4 * np.abs(w), 2.0 ** -10 * s) + sl[t:t + m, h]
+                            assert np.all(np.isnan(w) == np.isnan(g))
+                            assert np.all((np.abs(g - w) <= ok) | np.isnan(w))
+                        # slots behind the last token keep their codes
+                        code = lambda pools: pools.view(torch.uint8)[pid, h, first + m:]
+                        assert torch.equal(code(getattr(cache, name)), code(before[name + "_codes"]))
+                    else:
+                        assert np.array_equal(got[pid, h, :first], held[pid, h, :first], equal_nan=True)
+                        assert np.array_equal(got[pid, h, first + m:], held[pid, h, first + m:], equal_nan=True)
+                        w, g = new[t:t + m, h], got[pid, h, first:first + m]
+                        assert np.all(np.abs(g - w) <= 2.0 ** -8 * np.abs(w) + sl[t:t + m, h])
+                t += m
+    for name in "KV":
+        for pid in range(cache.K.shape[0]):
+            if pid not in touched:
+                assert torch.equal(getattr(cache, name)[pid].view(torch.uint8),
+                                   before[name + "_codes"][pid].view(torch.uint8))
+                if cache.scaled:
+                    assert np.array_equal(getattr(cache, name + "_scale")[pid].cpu().numpy(),
+                                          before[name + "_scale"][pid])
+
+
+def _snapshot(cache):
+    s = {}
+    for name in "KV":
+        s[name] = _values(cache, name)
+        s[name + "_codes"] = getattr(cache, name).clone()
+        if cache.scaled:
+            s[name + "_scale"] = getattr(cache, name + "_scale").cpu().numpy().copy()
+    return s
+
+
+WRITES = [
+    # lens, first positions, hkv, hq, d, page, pages, io, rot, interleaved
+    ([1], [0], 1, 0, 64, 16, E4, BF, 0, False),
+    ([1, 1, 1, 1], [10_000_003, 10_000_063, 9_999_999, 10_000_064], 1, 16, 128, 64, E4, BF, 128, False),
+    ([17], [0], 2, 2, 64, 16, E4, F32, 64, True),
+    ([33, 0, 5, 1], [15, 16, 31, 200], 3, 6, 128, 32, E4, BF, 48, False),
+    ([40, 3], [127, 1], 4, 4, 64, 128, E4, F32, 16, False),
+    ([300, 2, 0, 131], [5, 0, 0, 66], 2, 10, 128, 64, E4, BF, 128, True),
+    ([50, 7], [9, 100], 2, 4, 128, 16, BF, BF, 128, False),
+    ([50, 7], [9, 100], 2, 4, 64, 16, BF, F32, 32, True),
+    ([9], [3], 40, 48, 64, 16, E4, BF, 64, False),
+    ([1] * 70, list(range(70)), 2, 2, 64, 32, E4, BF, 64, False),
+]
+
+
+@pytest.mark.parametrize("lens,pos0,hkv,hq,d,page,dtype,io,rot,inter", WRITES)
+def test_write_matches_the_float64_statement(lens, pos0, hkv, hq, d, page, dtype, io, rot, inter):
+    B = len(lens)
+    # the table covers far positions; only the pages from the first position on exist
+    last = max(p + n for p, n in zip(pos0, lens))
+    near = _shuffled_cache(B, page * (max((p % page + n + page - 1) // page for p, n in zip(pos0, lens)) + 1), hkv, d,
+                           page, dtype, 1)
+    table = torch.full((B, last // page + 2), -1, dtype=torch.int32, device="cuda")
+    for b in range(B):
+        k = pos0[b] // page
+        w = min(near.page_table.shape[1], table.shape[1] - k)
+        table[b, k:k + w] = near.page_table[b, :w]
+    cache = lsa.KVCache(near.K, near.V, table, near.K_scale, near.V_scale)
+    pos = torch.tensor(pos0, dtype=torch.int64, device="cuda")
+    for step, f in ((0, 1.0), (1, 300.0), (2, 0.01)):
+        # three writes in a row: the second one's values are larger, so a part-filled page changes its scale
+        K, V, Q, cu = _new_tokens(lens, hkv, hq, d, io, 10 + step, pad=3, loud=[(i, f) for i in range(sum(lens))])
+        before = _snapshot(cache)
+        if step == 0 and cache.scaled:
+            for name in "KV":        # what a page held before has no codes that are NaN
+                p = getattr(cache, name).view(torch.uint8)
+                p.copy_(torch.where((p & 0x7f) == 0x7f, p & 0x80, p))
+            before = _snapshot(cache)
+        K_out = torch.full_like(K, 7.0)
+        Q_out = torch.full_like(Q, 7.0) if hq else None
+        lsa.lsa_cache_write(cache, K, V, cu, pos, Q=Q, inv_freq=_inv_freq(rot), interleaved=inter, K_out=K_out,
+                            Q_out=Q_out)
+        assert lsa.lsa_check() == lsa.LSA_OK
+        _check_write(cache, before, K, V, Q, K_out, Q_out, cu, pos, rot, inter)
+        n = sum(lens)
+        assert torch.all(K_out[n:] == 7.0) and (not hq or torch.all(Q_out[n:] == 7.0))
+
+
+def test_write_in_place_and_without_outputs_leaves_the_same_pages():
+    lens, pos0 = [37, 5], [11, 60]
+    K, V, Q, cu = _new_tokens(lens, 2, 4, 128, BF, 3)
+    pos, f = torch.tensor(pos0, device="cuda"), _inv_freq(128)
+    pools = []
+    for mode in range(3):
+        c = _shuffled_cache(2, 128, 2, 128, 32, E4, 5)
+        k, q = K.clone(), Q.clone()
+        if mode == 0:
+            q, k = lsa.lsa_cache_write(c, k, V, cu, pos, Q=q, inv_freq=f, want_K=True)
+        elif mode == 1:
+            lsa.lsa_cache_write(c, k, V, cu, pos, Q=q, inv_freq=f, K_out=k, Q_out=q)
+        else:
+            assert lsa.lsa_cache_write(c, k, V, cu, pos, inv_freq=f) == (None, None)
+            k, q = pools[0][0], pools[0][1]
+        pools.append((k, q, c.K.view(torch.uint8), c.V.view(torch.uint8), c.K_scale, c.V_scale))
+    for p in pools[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(p, pools[0]))
+
+
+def test_write_values_that_are_not_finite_or_too_large():
+    c = lsa.make_kv_cache(1, 32, 1, 64, page=16)
+    K, V, _, cu = _new_tokens([20], 1, 0, 64, F32, 4)
+    V[3, 0, 5], V[3, 0, 6], V[4, 0, 7], V[17, 0, 0] = math.inf, -math.inf, math.nan, 3e38
+    K[2, 0, 1] = math.nan
+    before = _snapshot(c)
+    lsa.lsa_cache_write(c, K, V, cu, torch.zeros(1, dtype=torch.int64, device="cuda"))
+    assert lsa.lsa_check() == lsa.LSA_OK
+    got = _values(c, "V")[0, 0]
+    assert np.isnan(got[3, 5]) and np.isnan(got[3, 6]) and np.isnan(got[4, 7]) and np.isnan(got).sum() == 3
+    assert np.isnan(_values(c, "K")[0, 0]).sum() == 1
+    assert c.V_scale[0, 0] <= 1 and c.V_scale[1, 0] == 2.0 ** 64        # only the finite ones count; clamped
+    assert _values(c, "V")[1, 0, 1, 0] == 448 * 2.0 ** 64               # saturates
+    _check_write(c, before, K, V, None, None, None, cu, torch.zeros(1, dtype=torch.int64), 0, False)
+
+
+def test_write_latches_bad_pages_and_offsets():
+    f = _inv_freq(64)
+    K, V, Q, cu = _new_tokens([20, 20], 2, 2, 64, BF, 6)
+    pos = torch.tensor([0, 0], device="cuda")
+    for what in ("page id", "page id past the pool", "past the table", "negative position", "cu falls", "cu too long"):
+        c = _shuffled_cache(2, 32, 2, 64, 16, E4, 7)
+        ref = _shuffled_cache(2, 32, 2, 64, 16, E4, 7)
+        lsa.lsa_cache_write(ref, K, V, cu, pos, Q=Q, inv_freq=f)
+        assert lsa.lsa_check() == lsa.LSA_OK
+        untouched = _snapshot(c)["K_codes"].view(torch.uint8)
+        p, q, bad = pos.clone(), cu.clone(), None
+        if what == "page id":
+            bad, c.page_table[1, 1] = (1, 1), -1
+        elif what == "page id past the pool":
+            bad, c.page_table[0, 0] = (0, 0), c.K.shape[0]
+        elif what == "past the table":
+            p[1] = 16
+        elif what == "negative position":
+            p[1] = -1
+        elif what == "cu falls":
+            q[1] = 45
+        else:
+            q[2] = 41
+        lsa.lsa_cache_write(c, K, V, q, p, Q=Q, inv_freq=f)
+        assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+        assert lsa.lsa_check() == lsa.LSA_OK
+        now = c.K.view(torch.uint8)
+        if what.startswith("cu"):
+            assert torch.equal(now, untouched)
+        elif bad:        # the other pages are as they should be
+            for b in range(2):
+                for j in range(2):
+                    pid = int(ref.page_table[b, j])
+                    want = untouched[pid] if (b, j) == bad else ref.K.view(torch.uint8)[pid]
+                    assert torch.equal(now[pid], want)
+
+
+def test_write_refuses_what_it_cannot_take():
+    c = lsa.make_kv_cache(1, 32, 1, 64, page=16)
+    K, V, Q, cu = _new_tokens([4], 1, 1, 64, BF, 6)
+    pos = torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        lsa.lsa_cache_write(c, K, torch.cat([V, V], 2)[..., ::2], cu, pos)
+    flat = torch.zeros(4 * 64 + 8, dtype=BF, device="cuda")
+    with pytest.raises(lsa.LsaError):           # not on a 16-byte boundary
+        lsa.lsa_cache_write(c, flat[1:257].view(4, 1, 64), V, cu, pos)
+    with pytest.raises(ValueError, match="the cache on"):
+        lsa.lsa_cache_write(c, K.cpu(), V.cpu(), cu, pos)
+    # no token at all
+    lsa.lsa_cache_write(c, K[:0], V[:0], cu * 0, pos)
+    assert lsa.lsa_check() == lsa.LSA_OK
+
+
+# ------------------------------------------------------------------ attention
+def _filled(batch, tokens, hkv, d, page, dtype, seed, spread=0):
+    """A cache full of values; `spread`: page scales up to 2^spread apart, the values' sizes unchanged for K and
+    following the scale for V."""
+    c = _shuffled_cache(batch, tokens, hkv, d, page, dtype, seed)
+    g = _gen(seed + 1)
+    for name in "KV":
+        x = torch.randn(c.K.shape, generator=g, device="cuda")
+        pool, scale = getattr(c, name), getattr(c, name + "_scale")
+        if scale is None:
+            pool.copy_(x.to(dtype))
+            continue
+        e = torch.randint(-spread, spread + 1, scale.shape, generator=g, device="cuda").float()
+        s = torch.exp2(e - 6)
+        scale.copy_(s)
+        y = x / (s[:, :, None, None] if name == "K" and spread <= 6 else 2.0 ** -6)
+        pool.copy_(y.clamp(-440, 440).to(dtype))
+    return c
+
+
+def _selection(g, batch, nq, hkv, max_sel, tokens, lengths):
+    """Rows of `lengths` distinct ascending tokens, entries behind them garbage."""
+    n = batch * nq * hkv
+    idx = np.full((n, max_sel), 2 ** 31 - 1, dtype=np.int64)
+    idx[:, 1::2] = -12345
+    cnt = np.array([lengths[i % len(lengths)] for i in range(n)])
+    for i in range(n):
+        idx[i, :cnt[i]] = np.sort(g.choice(tokens, size=cnt[i], replace=False))
+    to = lambda a, *s: torch.tensor(a, dtype=torch.int32, device="cuda").view(*s)
+    return to(idx, batch, nq, hkv, max_sel), to(cnt, batch, nq, hkv)
+
+
+def _check_attn(cache, Q, idx, cnt, Oo, lse):
+    """Against float64 softmax attention over the cache's values, row by row."""
+    B, nq, hq, d = Q.shape
+    G = hq // cache.hkv
+    vals = {n: _values(cache, n) for n in "KV"}
+    table = cache.page_table.cpu().numpy()
+    q, o, z = Q.double().cpu().numpy(), Oo.double().cpu().numpy(), lse.cpu().numpy()
+    idx, cnt = idx.cpu().numpy(), cnt.cpu().numpy()
+    worst = 0.0
+    for b in range(B):
+        for i in range(nq):
+            for h in range(cache.hkv):
+                n = cnt[b, i, h]
+                hs = slice(h * G, (h + 1) * G)
+                if n == 0:
+                    assert np.all(o[b, i, hs] == 0) and np.all(z[b, i, hs] == -np.inf)
+                    continue
+                t = idx[b, i, h, :n]
+                k, v = (vals[x][table[b, t // cache.page], h, t % cache.page] for x in "KV")
+                s = q[b, i, hs] @ k.T / math.sqrt(d)
+                m = s.max(1, keepdims=True)
+                p = np.exp(s - m)
+                want = p @ v / p.sum(1, keepdims=True)
+                wz = (m + np.log(p.sum(1, keepdims=True)))[:, 0]
+                # a score: d products summed in fp32 (each within 2^-24 of the sum of magnitudes), the scale and the
+                # base-2 exponent; a weight is off by that much relative, the sums by 2^-24 an addition
+                ds = 2.0 ** -24 * (d + 8) * (np.abs(q[b, i, hs]) @ np.abs(k).T).max(1) / math.sqrt(d) + 2.0 ** -21
+                spread = (p @ np.abs(v)) / p.sum(1, keepdims=True)       # what the weights' errors act on
+                # weights rounded to 11 bits where they meet the tensor cores, to 2^-25 of the largest at least
+                w11 = 2.0 ** -11 if Q.dtype == BF else 0.0
+                tol = spread * (2 * ds[:, None] + 2.0 ** -23 * n + w11)
+                if Q.dtype == BF:
+                    tol = tol + 2.0 ** -25 * n * np.abs(v).max(0) / p.sum(1, keepdims=True)
+                tol = tol + HALF_STEP[Q.dtype] * np.abs(want) + 1e-30
+                err = np.abs(o[b, i, hs] - want)
+                assert np.all(err <= tol), (b, i, h, n, float((err / tol).max()))
+                worst = max(worst, float((err / tol).max()))
+                assert np.all(np.abs(z[b, i, hs] - wz) <= ds + 2.0 ** -23 * (n + np.abs(wz)))
+    return worst
+
+
+ATTN = [
+    # batch, nq, hq, hkv, d, page, pages, io, max_sel, tokens, lengths
+    (1, 1, 1, 1, 64, 16, E4, BF, 1, 1, [1]),
+    (1, 1, 16, 1, 128, 64, E4, BF, 900, 5000, [900]),
+    (2, 3, 8, 2, 128, 32, E4, BF, 333, 700, [0, 1, 15, 16, 17, 333]),
+    (2, 3, 8, 2, 64, 16, E4, BF, 333, 700, [333, 0, 31, 32, 33, 2]),
+    (2, 2, 12, 4, 128, 128, BF, BF, 150, 300, [150, 0, 7, 64]),
+    (2, 2, 12, 4, 64, 16, BF, BF, 150, 300, [150, 0, 7, 64]),
+    (1, 2, 5, 1, 128, 64, E4, BF, 65, 129, [65, 64]),
+    (1, 3, 40, 2, 128, 64, E4, BF, 100, 200, [100, 3, 0]),
+    (1, 2, 64, 1, 64, 32, BF, BF, 100, 200, [100, 99]),
+    (2, 3, 6, 2, 128, 32, E4, F32, 200, 400, [200, 0, 1, 33]),
+    (1, 2, 10, 1, 64, 16, BF, F32, 77, 100, [77, 76]),
+    (1, 70, 8, 4, 64, 64, E4, BF, 48, 500, [48, 0, 47, 1]),
+    (3, 1, 16, 4, 128, 64, E4, BF, 3001, 4000, [3001, 2999, 0]),
+    (3, 400, 4, 1, 64, 64, E4, BF, 40, 500, [40, 0, 39, 1, 17]),
+]
+
+
+@pytest.mark.parametrize("batch,nq,hq,hkv,d,page,dtype,io,max_sel,tokens,lengths", ATTN)
+def test_attention_matches_float64(batch, nq, hq, hkv, d, page, dtype, io, max_sel, tokens, lengths):
+    c = _filled(batch, tokens, hkv, d, page, dtype, 20)
+    Q = torch.randn(batch, nq, hq, d, generator=_gen(21), device="cuda").to(io)
+    idx, cnt = _selection(np.random.RandomState(22), batch, nq, hkv, max_sel, tokens, lengths)
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    print("worst error over its bound: %.3f" % _check_attn(c, Q, idx, cnt, Oo, lse))
+    again, none = lsa.lsa_cache_attn(c, Q, idx, cnt, want_lse=False)
+    assert none is None and torch.equal(again, Oo)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("spread", [6, 30])
+def test_attention_with_scales_far_apart(io, spread):
+    """V scales 2^(2 spread) apart within a row (K's follow their values up to 2^6, scores beyond that are decided by
+    the largest page)."""
+    c = _filled(1, 600, 2, 128, 32, E4, 30, spread=spread)
+    if spread > 6:
+        c.K_scale.fill_(2.0 ** -6)
+    Q = torch.randn(1, 2, 8, 128, generator=_gen(31), device="cuda").to(io)
+    idx, cnt = _selection(np.random.RandomState(32), 1, 2, 2, 300, 600, [300, 17])
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    _check_attn(c, Q, idx, cnt, Oo, lse)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_attention_with_large_scores_and_queries(io):
+    """Scores of thousands (one key takes all the weight) and queries near the type's ends."""
+    c = _filled(1, 100, 1, 64, 16, E4, 33)
+    idx, cnt = _selection(np.random.RandomState(34), 1, 3, 1, 60, 100, [60, 59, 1])
+    Q = torch.randn(1, 3, 4, 64, generator=_gen(35), device="cuda")
+    Q[:, 0] *= 1e3
+    Q[:, 1] *= 1e-30
+    Q[:, 2, 1:] = 0
+    Q = Q.to(io)
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    _check_attn(c, Q, idx, cnt, Oo, lse)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_attention_any_order_repeats_and_what_is_not_selected(io):
+    """A token may stand in a row twice (it counts twice), in any order; NaN in slots that no row selects, and in
+    entries of the table that no row reaches, are not read."""
+    c = _filled(1, 200, 1, 64, 16, E4, 40)
+    row = torch.tensor([7, 150, 7, 3, 3, 3, 199, 0], dtype=torch.int32, device="cuda")
+    idx = row.view(1, 1, 1, -1).expand(1, 2, 1, -1).contiguous()
+    cnt = torch.tensor([8, 3], dtype=torch.int32, device="cuda").view(1, 2, 1)
+    keep = torch.zeros(200, dtype=torch.bool)
+    keep[row.long().cpu()] = True
+    for t in range(200):
+        if not keep[t]:
+            pid = int(c.page_table[0, t // 16])
+            c.K.view(torch.uint8)[pid, :, t % 16] = 0x7f
+            c.V.view(torch.uint8)[pid, :, t % 16] = 0xff
+    c.page_table[0, 5] = -7
+    Q = torch.randn(1, 2, 4, 64, generator=_gen(41), device="cuda").to(io)
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    _check_attn(c, Q, idx, cnt, Oo, lse)
+    # a selected NaN reaches its heads, and no other row
+    c.K.view(torch.uint8)[int(c.page_table[0, 0]), 0, 0] = 0x7f
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert torch.isnan(Oo[0, 0]).all() and torch.isnan(lse[0, 0]).all()
+    assert torch.isfinite(Oo[0, 1].float()).all() and torch.isfinite(lse[0, 1]).all()
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_attention_skips_and_latches_bad_tokens(io):
+    c = _filled(2, 64, 1, 64, 16, E4, 50)
+    Q = torch.randn(2, 1, 4, 64, generator=_gen(51), device="cuda").to(io)
+    good = torch.tensor([1, 5, 20, 40], dtype=torch.int32, device="cuda")
+    idx = good.view(1, 1, 1, 4).expand(2, 1, 1, 4).contiguous()
+    cnt = torch.full((2, 1, 1), 4, dtype=torch.int32, device="cuda")
+    ref, rl = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    for bad in (-1, 64, 2 ** 31 - 1, -2 ** 31):
+        i2 = torch.cat([idx[..., :2], torch.full_like(idx[..., :1], bad), idx[..., 2:]], -1).contiguous()
+        Oo, lse = lsa.lsa_cache_attn(c, Q, i2, cnt + 1)
+        assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+        _check_attn(c, Q, idx, cnt, Oo, lse)
+    c.page_table[1, 1] = c.K.shape[0]
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+    assert torch.equal(Oo[0], ref[0])
+    # a count out of range is clamped and latched; all tokens bad gives the empty row
+    lsa.lsa_cache_attn(c, Q, idx, cnt * 2)
+    assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx * 0 - 1, cnt)
+    assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+    assert torch.all(Oo == 0) and torch.all(lse == -math.inf)
+
+
+def test_attention_refuses_what_it_cannot_take():
+    c = _filled(1, 64, 1, 64, 16, E4, 50)
+    idx = torch.zeros(1, 1, 1, 4, dtype=torch.int32, device="cuda")
+    cnt = torch.zeros(1, 1, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(lsa.LsaError):           # more than 64 heads share a row
+        lsa.lsa_cache_attn(c, torch.zeros(1, 1, 65, 64, dtype=BF, device="cuda"), idx, cnt)
+    flat = torch.zeros(68, dtype=BF, device="cuda")
+    with pytest.raises(lsa.LsaError):           # not on a 16-byte boundary
+        lsa.lsa_cache_attn(c, flat[1:65].view(1, 1, 1, 64), idx, cnt)
+    with pytest.raises(ValueError, match="contiguous"):
+        lsa.lsa_cache_attn(c, torch.zeros(1, 1, 2, 128, dtype=BF, device="cuda")[..., ::2], idx, cnt)
+    none = torch.zeros(1, 0, 4, 64, dtype=BF, device="cuda")
+    Oo, lse = lsa.lsa_cache_attn(c, none, idx[:, :0], cnt[:, :0])
+    assert Oo.shape == none.shape and lse.shape == (1, 0, 4)
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 2^31 elements: pages at both ends are written and read."""
+    page, hkv, d = 128, 8, 128
+    n_pages = 2 ** 31 // (page * hkv * d) + 64
+    K = torch.empty(n_pages, hkv, page, d, dtype=E4, device="cuda")
+    V = torch.empty(n_pages, hkv, page, d, dtype=E4, device="cuda")
+    assert K.numel() > 2 ** 31
+    s = torch.ones(n_pages, hkv, device="cuda")
+    table = torch.tensor([[0, n_pages - 1, n_pages - 2, 5]], dtype=torch.int32, device="cuda")
+    big = lsa.KVCache(K, V, table, s, s.clone())
+    small = lsa.make_kv_cache(1, 512, hkv, d, page)
+    Kn, Vn, Qn, cu = _new_tokens([500], hkv, 16, d, BF, 60)
+    pos = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for c in (big, small):
+        q, _ = lsa.lsa_cache_write(c, Kn, Vn, cu, pos, Q=Qn, inv_freq=_inv_freq(128))
+    for i, pid in enumerate(table[0].tolist()):
+        m = min(page, 500 - i * page)
+        assert torch.equal(K[pid, :, :m].view(torch.uint8), small.K[i, :, :m].view(torch.uint8))
+        assert torch.equal(V[pid, :, :m].view(torch.uint8), small.V[i, :, :m].view(torch.uint8))
+    idx, cnt = _selection(np.random.RandomState(61), 1, 4, hkv, 300, 500, [300])
+    Q = q[-4:].reshape(1, 4, 16, d).contiguous()
+    a, b = lsa.lsa_cache_attn(big, Q, idx, cnt), lsa.lsa_cache_attn(small, Q, idx, cnt)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert lsa.lsa_check() == lsa.LSA_OK
+
+
+def test_two_streams_and_two_replayed_graphs():
+    """Two caches served on two streams at once, eagerly and from captured graphs whose inputs change between
+    replays, give the bits of calls made one after another."""
+    sets = []
+    for k in range(2):
+        K, V, Q, cu = _new_tokens([9, 30], 2, 8, 128, BF, 70 + k)
+        sets.append(dict(cache=_filled(2, 128, 2, 128, 32, E4, 72 + k), K=K, V=V, Q=Q, cu=cu, f=_inv_freq(128),
+                         pos=torch.tensor([40, 64], device="cuda"), q=torch.empty_like(Q),
+                         O=torch.empty(2, 5, 8, 128, dtype=BF, device="cuda"),
+                         lse=torch.empty(2, 5, 8, device="cuda")))
+        sets[k]["idx"], sets[k]["cnt"] = _selection(np.random.RandomState(k), 2, 5, 2, 60, 90, [60, 5, 0])
+
+    def step(s):
+        lsa.lsa_cache_write(s["cache"], s["K"], s["V"], s["cu"], s["pos"], Q=s["Q"], inv_freq=s["f"], Q_out=s["q"])
+        lsa.lsa_cache_attn(s["cache"], s["q"][:10].view(2, 5, 8, 128), s["idx"], s["cnt"], O=s["O"], lse=s["lse"])
+
+    def state(s):
+        c = s["cache"]
+        return [t.clone() for t in (s["O"], s["lse"], s["q"], c.K.view(torch.uint8), c.V.view(torch.uint8), c.K_scale,
+                                    c.V_scale)]
+
+    start = [state(s) for s in sets]
+
+    def reset():
+        for s, st in zip(sets, start):
+            c = s["cache"]
+            for t, v in zip((c.K.view(torch.uint8), c.V.view(torch.uint8), c.K_scale, c.V_scale), st[3:]):
+                t.copy_(v)
+
+    want = []
+    for s in sets:
+        step(s)
+        want.append(state(s))
+    reset()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s, st in zip(sets, streams):
+        with torch.cuda.stream(st):
+            step(s)
+    torch.cuda.synchronize()
+    for s, w in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(state(s), w))
+    graphs = []
+    for s, st in zip(sets, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            step(s)
+        graphs.append(g)
+    saved = [s["K"].clone() for s in sets]
+    for s in sets:       # other inputs in the same buffers, then the first ones again
+        s["K"].mul_(-2)
+    for round_ in range(2):
+        reset()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for k, s in enumerate(sets):
+            same = all(torch.equal(a, b) for a, b in zip(state(s), want[k]))
+            assert same == (round_ == 1)
+            s["K"].copy_(saved[k])
+        torch.cuda.synchronize()
+    assert lsa.lsa_check() == lsa.LSA_OK
+    del graphs
+
+
+# ------------------------------------------------------ the calls as they are used together
+def _served(dtype, seed=80, n0=2000, steps=40, hkv=2, hq=8, d=64):
+    """A prompt and decode tokens, and a cache they have been written into."""
+    lens = [n0, n0]
+    K, V, Q, _ = _new_tokens([2 * (n0 + steps)], hkv, hq, d, BF, seed)
+    B = 2
+    K, V, Q = (t.view(B, n0 + steps, -1, d) for t in (K, V, Q))
+    cache = _shuffled_cache(B, n0 + steps, hkv, d, 32, dtype, seed + 1)
+    return K, V, Q, cache
+
+
+@pytest.mark.parametrize("dtype", [E4, BF])
+def test_prompt_then_decode_from_the_cache(dtype):
+    """Write the prompt, build the index of its rotated keys, then decode: write, index, select, attend.  The index
+    and the selections equal, bit for bit, those kept up from dense keys that hold the cache's values; the attention
+    is checked against float64 at every step."""
+    n0, steps, hkv, hq, d, pool, sink, window, topk = 2000, 40, 2, 8, 64, 4, 8, 64, 256
+    K, V, Q, cache = _served(dtype)
+    B, f = 2, _inv_freq(d)
+    dev = K.device
+    cu = torch.tensor([0, n0, 2 * n0], dtype=torch.int64, device=dev)
+    flat = lambda t, a, b: t[:, a:b].reshape(-1, t.shape[2], d).contiguous()
+    _, k_rot = lsa.lsa_cache_write(cache, flat(K, 0, n0), flat(V, 0, n0), cu, torch.zeros(B, dtype=torch.int64,
+                                   device=dev), Q=flat(Q, 0, n0), inv_freq=f, want_K=True)
+    ld = n0 + steps
+    W = torch.linalg.qr(torch.randn(d, d, generator=_gen(90), device=dev))[0][:, :32].contiguous()
+    dense = torch.zeros(B, ld, hkv, d, device=dev)
+
+    def from_cache(a, b):
+        """The cache's keys of tokens [a, b) as fp32 [B, b - a, hkv, d]."""
+        t = torch.arange(a, b, device=dev)
+        pid = cache.page_table[:, t // cache.page].long()
+        x = cache.K.view(torch.uint8 if cache.scaled else BF)[pid, :, t % cache.page]
+        if not cache.scaled:
+            return x.float()
+        return x.view(E4).float() * cache.K_scale[pid][..., None]
+
+    dense[:, :n0] = k_rot.view(B, n0, hkv, d).float()
+    mk = lambda dt: lsa.make_build_params(B, n0, ld, hkv, d, 32, pool, dt, (8, 64), 3, 0, sink, steps)
+    mine = lsa.lsa_build_index(mk(lsa.LSA_BF16), dense.to(BF), W)
+    ref = lsa.lsa_build_index(mk(lsa.LSA_F32), dense, W)      # the same keys; fp32, so that it can hold 8-bit values
+    sp = lsa.make_select_params(hq, 16, topk, sink, window)
+    one = torch.arange(B + 1, dtype=torch.int64, device=dev)
+    for i in range(n0, n0 + steps):
+        pos = torch.full((B,), i, dtype=torch.int64, device=dev)
+        q, _ = lsa.lsa_cache_write(cache, flat(K, i, i + 1), flat(V, i, i + 1), one, pos, Q=flat(Q, i, i + 1),
+                                   inv_freq=f)
+        lsa.lsa_append_cached(mine, cache, 1)
+        if (i + 1) % pool == 0:
+            dense[:, i + 1 - pool:i + 1] = from_cache(i + 1 - pool, i + 1)
+        lsa.lsa_append(ref, dense, 1)
+        q = q.view(B, 1, hq, d)
+        idx, cnt = lsa.lsa_select(mine, sp, q, q_pos0=i)
+        ridx, rcnt = lsa.lsa_select(ref, sp, q.float(), q_pos0=i)
+        assert torch.equal(idx, ridx) and torch.equal(cnt, rcnt)
+        Oo, lse = lsa.lsa_cache_attn(cache, q, idx, cnt)
+        if i % 8 == 0 or i > n0 + steps - 3:
+            _check_attn(cache, q, idx, cnt, Oo, lse)
+    assert torch.equal(mine.get(lsa.LSA_GET_LATENT), ref.get(lsa.LSA_GET_LATENT))
+    assert torch.equal(mine.get(lsa.LSA_GET_LEAF_OF_BLOCK), ref.get(lsa.LSA_GET_LEAF_OF_BLOCK))
+    assert lsa.lsa_check(mine) == lsa.lsa_check(ref) == lsa.lsa_check() == lsa.LSA_OK
+    mine.free()
+    ref.free()
+
+
+def test_append_cached_latches_missing_pages():
+    K, V, Q, cache = _served(BF, n0=64, steps=16)
+    k = K[:, :64].contiguous()
+    bp = lsa.make_build_params(2, 64, 80, 2, 64, 16, 4, lsa.LSA_BF16, (4,), 2, 0, 0, 16)
+    ix = lsa.lsa_build_index(bp, torch.cat([k, K[:, 64:]], 1).contiguous(), torch.eye(64, device="cuda")[:, :16]
+                             .contiguous())
+    cache.page_table[1, 2] = -1
+    lsa.lsa_append_cached(ix, cache, 4)
+    assert lsa.lsa_check(ix) == lsa.LSA_ERR_DEVICE
+    with pytest.raises(lsa.LsaError):           # past the append capacity
+        lsa.lsa_append_cached(ix, cache, 13)
+    ix.free()
