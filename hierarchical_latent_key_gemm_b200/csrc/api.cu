@@ -398,6 +398,7 @@ bool valid_cache(const lsa_kv_cache* c) {
     // page ids are int32; the last token of a row of the table stays within int32
     if (c->n_pages > INT32_MAX || c->ld_pages > ((int64_t)1 << 31) / c->page || c->batch > 65535 || c->hkv > 4096)
         return false;
+    if (c->n_pages * c->hkv * c->page >= 0xffffffffll) return false;   // rows of the pools are uint32
     if (!is_here(c->K) || !is_here(c->V) || !is_here(c->page_table)) return false;
     if (!aligned16(c->K) || !aligned16(c->V)) return false;
     return c->dtype != LSA_E4M3 || (is_here(c->K_scale) && is_here(c->V_scale));
