@@ -549,6 +549,23 @@ def lsa_merge_attn(O_parts, lse_parts, O=None, lse=None, want_lse=True, stream=N
 
 
 # ------------------------------------------------------------ paged KV cache
+def _cuda_arg(t, shape, dtype, index, name):
+    """Address of a tensor argument (None: null) after the checks that the C
+    call cannot make: its shape, element type, device and layout.  One function
+    with little in it: a decode step's kernels take a few microseconds."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on CUDA device {index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 class KVCache:
     """A paged cache of keys and values (lsa_kv_cache) over the caller's
     tensors: pools K, V [n_pages, hkv, page, d], bfloat16 or float8_e4m3fn, the
@@ -558,30 +575,34 @@ class KVCache:
     server updates page_table in place as it hands out pages."""
 
     def __init__(self, K, V, page_table, K_scale=None, V_scale=None):
-        if K.dim() != 4 or page_table.dim() != 2:
+        shape, dtype, index = K.shape, K.dtype, K.get_device()
+        if len(shape) != 4 or page_table.dim() != 2:
             raise ValueError("K and V must be [n_pages, hkv, page, d] and page_table [batch, ld_pages]")
-        n_pages, hkv, page, d = K.shape
-        if K.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or V.dtype != K.dtype:
-            raise ValueError(f"K and V must both be bfloat16 or float8_e4m3fn, got {K.dtype} and {V.dtype}")
-        _shape(V, K.shape, "V")
-        self.scaled = K.dtype == torch.float8_e4m3fn
-        if self.scaled:
+        n_pages, hkv, page, d = shape
+        self.batch, ld_pages = table = page_table.shape
+        if dtype is torch.float8_e4m3fn:
+            code = LSA_E4M3
             if K_scale is None or V_scale is None:
                 raise ValueError("float8 pages need K_scale and V_scale")
-            _shape(K_scale, (n_pages, hkv), "K_scale")
-            _shape(V_scale, (n_pages, hkv), "V_scale")
-        elif K_scale is not None or V_scale is not None:
-            raise ValueError("bfloat16 pages have no scales")
+        elif dtype is torch.bfloat16:
+            code = LSA_BF16
+            if K_scale is not None or V_scale is not None:
+                raise ValueError("bfloat16 pages have no scales")
+        else:
+            raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, got {dtype}")
         if page not in (16, 32, 64, 128) or d not in (64, 128):
             raise ValueError(f"pages hold 16, 32, 64 or 128 tokens of 64 or 128 components, got {page} and {d}")
+        scales = (n_pages, hkv)
         self.K, self.V, self.page_table, self.K_scale, self.V_scale = K, V, page_table, K_scale, V_scale
-        self.device = K.device
-        _on_device(self.device, V=V, page_table=page_table, K_scale=K_scale, V_scale=V_scale)
-        self.batch, self.hkv, self.page, self.d = page_table.shape[0], hkv, page, d
-        self.desc = KVCacheDesc(n_pages, self.batch, page_table.shape[1], page, hkv, d,
-                                LSA_E4M3 if self.scaled else LSA_BF16, _ptr(K), _ptr(V),
-                                _typed(K_scale, torch.float32, "K_scale"), _typed(V_scale, torch.float32, "V_scale"),
-                                _typed(page_table, torch.int32, "page_table"))
+        self.index, self.hkv, self.page, self.d, self.scaled = index, hkv, page, d, code == LSA_E4M3
+        self.desc = KVCacheDesc(n_pages, self.batch, ld_pages, page, hkv, d, code,
+                                _cuda_arg(K, shape, dtype, index, "K"), _cuda_arg(V, shape, dtype, index, "V"),
+                                _cuda_arg(K_scale, scales, torch.float32, index, "K_scale"),
+                                _cuda_arg(V_scale, scales, torch.float32, index, "V_scale"),
+                                _cuda_arg(page_table, table, torch.int32, index, "page_table"))
+        if index < 0:
+            raise ValueError("the cache must live on a CUDA device")
+        self.ref = C.byref(self.desc)
 
 
 def make_kv_cache(batch, max_tokens, hkv, d, page=64, dtype=torch.float8_e4m3fn, n_pages=None, device="cuda"):
@@ -601,10 +622,20 @@ def make_kv_cache(batch, max_tokens, hkv, d, page=64, dtype=torch.float8_e4m3fn,
     return KVCache(pools[0], pools[1], table, scales[0], scales[1])
 
 
-def _on_device(device, **ts):
-    for name, t in ts.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+_IO_CODES = {torch.float32: LSA_F32, torch.bfloat16: LSA_BF16}
+
+
+def _io_code(t):
+    code = _IO_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _cache_stream(cache, stream):
+    if stream is None:
+        return torch.cuda.current_stream(cache.index).cuda_stream
+    return _stream(stream)
 
 
 def lsa_cache_write(cache: KVCache, K, V, cu, pos0, Q=None, inv_freq=None, interleaved=False, K_out=None, Q_out=None,
@@ -616,40 +647,32 @@ def lsa_cache_write(cache: KVCache, K, V, cu, pos0, Q=None, inv_freq=None, inter
     Returns (Q_out, K_out): the rotated queries (None without Q) and, when
     K_out is given or want_K is set, the rotated keys.  K_out may be K, Q_out
     may be Q."""
-    if K.dim() != 3:
-        raise ValueError(f"K must be [n, hkv, d], got shape {tuple(K.shape)}")
-    n, hq = K.shape[0], 0
-    _shape(K, (n, cache.hkv, cache.d), "K")
-    _shape(V, K.shape, "V")
-    _shape(cu, (cache.batch + 1,), "cu")
-    _shape(pos0, (cache.batch,), "pos0")
-    if Q is not None:
-        if Q.dim() != 3:
-            raise ValueError(f"Q must be [n, hq, d], got shape {tuple(Q.shape)}")
-        hq = Q.shape[1]
-        _shape(Q, (n, hq, cache.d), "Q")
-        if Q_out is None:
-            Q_out = torch.empty_like(Q)
-        _shape(Q_out, Q.shape, "Q_out")
-    elif Q_out is not None:
-        raise ValueError("Q_out without Q")
+    io, index, d, i64 = K.dtype, cache.index, cache.d, torch.int64
+    code = _io_code(K)
+    n, hq, rot = K.shape[0], 0, 0
+    kv, qs = (n, cache.hkv, d), None
     if K_out is None and want_K:
         K_out = torch.empty_like(K)
-    _shape(K_out, K.shape, "K_out")
-    rot = 0
+    if Q is not None:
+        hq = Q.shape[1]
+        qs = (n, hq, d)
+        if Q_out is None:
+            Q_out = torch.empty_like(Q)
+    elif Q_out is not None:
+        raise ValueError("Q_out without Q")
     if inv_freq is not None:
-        if inv_freq.dim() != 1:
-            raise ValueError(f"inv_freq must be [rot/2], got shape {tuple(inv_freq.shape)}")
         rot = 2 * inv_freq.shape[0]
-        if rot % 16 or rot > cache.d:
-            raise ValueError(f"the rotated components must be a multiple of 16 up to {cache.d}, got {rot}")
-    _same_dtype(K, V, Q, K_out, Q_out)
-    _on_device(cache.device, K=K, V=V, Q=Q, cu=cu, pos0=pos0, inv_freq=inv_freq, K_out=K_out, Q_out=Q_out)
-    st = lib().lsa_cache_write(C.byref(cache.desc), _ptr(K), _ptr(V), _ptr(Q), n, _typed(cu, torch.int64, "cu"),
-                               _typed(pos0, torch.int64, "pos0"), hq, dtype_code(K),
-                               _typed(inv_freq, torch.float64, "inv_freq"), rot, int(bool(interleaved)), _ptr(K_out),
-                               _ptr(Q_out), _stream(stream))
-    _ok(st, "lsa_cache_write")
+        if rot % 16 or rot > d:
+            raise ValueError(f"the rotated components must be a multiple of 16 up to {d}, got {rot}")
+    st = lib().lsa_cache_write(cache.ref, _cuda_arg(K, kv, io, index, "K"), _cuda_arg(V, kv, io, index, "V"),
+                               _cuda_arg(Q, qs, io, index, "Q"), n,
+                               _cuda_arg(cu, (cache.batch + 1,), i64, index, "cu"),
+                               _cuda_arg(pos0, (cache.batch,), i64, index, "pos0"), hq, code,
+                               _cuda_arg(inv_freq, (rot // 2,), torch.float64, index, "inv_freq"), rot,
+                               1 if interleaved else 0, _cuda_arg(K_out, kv, io, index, "K_out"),
+                               _cuda_arg(Q_out, qs, io, index, "Q_out"), _cache_stream(cache, stream))
+    if st != LSA_OK:
+        raise LsaError(st, "lsa_cache_write")
     return Q_out, K_out
 
 
@@ -657,27 +680,25 @@ def lsa_cache_attn(cache: KVCache, Q, idx, cnt, O=None, lse=None, want_lse=True,
     """lsa_sparse_attn with the selected rows read from the cache: Q [batch,
     nq, hq, d] float32 or bfloat16, idx [batch, nq, hkv, max_sel], cnt [batch,
     nq, hkv]; returns (O, lse)."""
-    if Q.dim() != 4:
-        raise ValueError(f"Q must be [batch, nq, hq, d], got shape {tuple(Q.shape)}")
-    B, nq, hq, d = Q.shape
-    _shape(Q, (cache.batch, nq, hq, cache.d), "Q")
-    if idx.dim() != 4:
-        raise ValueError(f"idx must be [batch, nq, hkv, max_sel], got shape {tuple(idx.shape)}")
+    io, index, i32 = Q.dtype, cache.index, torch.int32
+    code = _io_code(Q)
+    if Q.dim() != 4 or idx.dim() != 4:
+        raise ValueError("Q must be [batch, nq, hq, d] and idx [batch, nq, hkv, max_sel], got shapes "
+                         f"{tuple(Q.shape)} and {tuple(idx.shape)}")
+    batch, nq, hq, _ = Q.shape
     max_sel = idx.shape[3]
-    _shape(idx, (B, nq, cache.hkv, max_sel), "idx")
-    _shape(cnt, (B, nq, cache.hkv), "cnt")
+    shape, rows = (cache.batch, nq, hq, cache.d), (cache.batch, nq, cache.hkv)
     if O is None:
         O = torch.empty_like(Q)
     if lse is None and want_lse:
-        lse = torch.empty((B, nq, hq), dtype=torch.float32, device=Q.device)
-    _shape(O, Q.shape, "O")
-    _shape(lse, (B, nq, hq), "lse")
-    _same_dtype(Q, O)
-    _on_device(cache.device, Q=Q, idx=idx, cnt=cnt, O=O, lse=lse)
-    st = lib().lsa_cache_attn(C.byref(cache.desc), _ptr(Q), _typed(idx, torch.int32, "idx"),
-                              _typed(cnt, torch.int32, "cnt"), nq, hq, dtype_code(Q), max_sel, _ptr(O),
-                              _typed(lse, torch.float32, "lse"), _stream(stream))
-    _ok(st, "lsa_cache_attn")
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=Q.device)
+    st = lib().lsa_cache_attn(cache.ref, _cuda_arg(Q, shape, io, index, "Q"),
+                              _cuda_arg(idx, rows + (max_sel,), i32, index, "idx"),
+                              _cuda_arg(cnt, rows, i32, index, "cnt"), nq, hq, code, max_sel,
+                              _cuda_arg(O, shape, io, index, "O"),
+                              _cuda_arg(lse, shape[:3], torch.float32, index, "lse"), _cache_stream(cache, stream))
+    if st != LSA_OK:
+        raise LsaError(st, "lsa_cache_attn")
     return O, lse
 
 
@@ -687,7 +708,8 @@ def lsa_append_cached(index: Index, cache: KVCache, n_new: int, stream=None):
     if (cache.batch, cache.hkv, cache.d) != (p.batch, p.hkv, p.d):
         raise ValueError(f"the cache holds (batch, hkv, d) = {(cache.batch, cache.hkv, cache.d)}, the index "
                          f"{(p.batch, p.hkv, p.d)}")
-    _ok(lib().lsa_append_cached(index.handle, C.byref(cache.desc), int(n_new), _stream(stream)), "lsa_append_cached")
+    _ok(lib().lsa_append_cached(index.handle, cache.ref, int(n_new), _cache_stream(cache, stream)),
+        "lsa_append_cached")
 
 
 def _host_ptr(t, dtype, shape, name):

@@ -69,8 +69,8 @@ def test_cache_refuses_tensors_that_do_not_fit():
     s, tab = torch.ones(4, 2), torch.zeros(1, 3, dtype=torch.int32)
     cases = [
         (dict(V=V[:3]), "V must have shape"),
-        (dict(V=V.to(BF)), "both be"),
-        (dict(K=K.float(), V=V.float()), "both be"),
+        (dict(V=V.to(BF)), "V must be"),
+        (dict(K=K.float(), V=V.float()), "pages must be"),
         (dict(K_scale=None), "need K_scale"),
         (dict(V_scale=torch.ones(4, 3)), "V_scale must have shape"),
         (dict(K=K.to(BF), V=V.to(BF)), "no scales"),
@@ -89,8 +89,9 @@ def test_cache_refuses_tensors_that_do_not_fit():
 def _host_cache(hkv=2, d=64, batch=1):
     """A cache description over no memory: the calls must refuse before they use it."""
     c = lsa.KVCache.__new__(lsa.KVCache)
-    c.device, c.batch, c.hkv, c.page, c.d, c.scaled = torch.device("cpu"), batch, hkv, 16, d, True
+    c.index, c.batch, c.hkv, c.page, c.d, c.scaled = -1, batch, hkv, 16, d, True
     c.desc = lsa.KVCacheDesc(4, batch, 3, 16, hkv, d, lsa.LSA_E4M3)
+    c.ref = C.byref(c.desc)
     return c
 
 
@@ -100,13 +101,13 @@ def test_cache_write_checks_before_the_call():
     cu, pos0 = torch.zeros(2, dtype=torch.int64), torch.zeros(1, dtype=torch.int64)
     f = torch.ones(32, dtype=torch.float64)
     cases = [
-        (dict(K=K[0]), r"K must be \[n, hkv, d\]"),
+        (dict(K=K[0]), "K must have shape"),
         (dict(K=K[:, :1]), "K must have shape"),
         (dict(V=K[:4]), "V must have shape"),
-        (dict(V=K.float()), "share one dtype"),
+        (dict(V=K.float()), "V must be"),
         (dict(Q=Q[:4]), "Q must have shape"),
-        (dict(Q=Q[0]), r"Q must be \[n, hq, d\]"),
-        (dict(Q=Q.float()), "share one dtype"),
+        (dict(Q=Q[0]), "Q must have shape"),
+        (dict(Q=Q.float()), "Q must be"),
         (dict(Q=None, Q_out=Q), "Q_out without Q"),
         (dict(Q_out=Q[:, :2]), "Q_out must have shape"),
         (dict(K_out=K[:4]), "K_out must have shape"),
@@ -116,22 +117,23 @@ def test_cache_write_checks_before_the_call():
         (dict(pos0=pos0.int()), "pos0 must be"),
         (dict(inv_freq=f[:7]), "multiple of 16"),
         (dict(inv_freq=torch.ones(40, dtype=torch.float64)), "multiple of 16"),
-        (dict(inv_freq=f[None]), "inv_freq must be"),
+        (dict(inv_freq=f.view(32, 1)), "inv_freq must have shape"),
         (dict(inv_freq=f.float()), "inv_freq must be"),
         (dict(K=K.half(), V=K.half(), Q=Q.half()), "unsupported dtype"),
-        (dict(), "CUDA device"),
+        (dict(V=torch.cat([K, K], 2)[..., ::2]), "V must be contiguous"),
     ]
-    real = lsa._ptr
     for over, msg in cases:
         a = dict(K=K, V=K, cu=cu, pos0=pos0, Q=Q, inv_freq=f)
         a.update(over)
-        # the type checks run where pointers are taken: let them be, except in the last case
-        lsa._ptr = real if msg == "CUDA device" else (lambda t: None)
-        try:
-            with pytest.raises(ValueError, match=msg):
-                lsa.lsa_cache_write(_host_cache(), **a)
-        finally:
-            lsa._ptr = real
+        with pytest.raises(ValueError, match=msg):
+            lsa.lsa_cache_write(_host_cache(), **a, stream=0)
+    c = _host_cache()
+    c.index = 0
+    with pytest.raises(ValueError, match="K is on cpu, the cache on CUDA device 0"):
+        lsa.lsa_cache_write(c, K, K, cu, pos0, stream=0)
+    # well-formed, but the cache's own tensors are missing: the library refuses it
+    with pytest.raises(lsa.LsaError):
+        lsa.lsa_cache_write(_host_cache(), K, K, cu, pos0, stream=0)
 
 
 def test_cache_attn_checks_before_the_call():
@@ -142,27 +144,24 @@ def test_cache_attn_checks_before_the_call():
         (dict(Q=torch.zeros(2, 3, 4, 64, dtype=BF)), "Q must have shape"),
         (dict(Q=torch.zeros(1, 3, 4, 128, dtype=BF)), "Q must have shape"),
         (dict(idx=idx[:, :2]), "idx must have shape"),
-        (dict(idx=idx[0]), "idx must be"),
+        (dict(idx=idx[0]), r"idx \[batch, nq, hkv, max_sel\]"),
         (dict(idx=idx.long()), "idx must be"),
         (dict(cnt=cnt[..., None]), "cnt must have shape"),
         (dict(cnt=cnt.long()), "cnt must be"),
-        (dict(O=Q.float()), "share one dtype"),
+        (dict(O=Q.float()), "O must be"),
         (dict(O=Q[:, :2]), "O must have shape"),
         (dict(lse=torch.zeros(1, 3, 2)), "lse must have shape"),
         (dict(lse=torch.zeros(1, 3, 4, dtype=torch.float64)), "lse must be"),
         (dict(Q=Q.half()), "unsupported dtype"),
-        (dict(), "CUDA device"),
+        (dict(cnt=torch.zeros(1, 3, 4, dtype=torch.int32)[..., ::2]), "cnt must be contiguous"),
     ]
-    real = lsa._ptr
     for over, msg in cases:
         a = dict(Q=Q, idx=idx, cnt=cnt)
         a.update(over)
-        lsa._ptr = real if msg == "CUDA device" else (lambda t: None)
-        try:
-            with pytest.raises(ValueError, match=msg):
-                lsa.lsa_cache_attn(_host_cache(), **a)
-        finally:
-            lsa._ptr = real
+        with pytest.raises(ValueError, match=msg):
+            lsa.lsa_cache_attn(_host_cache(), **a, stream=0)
+    with pytest.raises(lsa.LsaError):
+        lsa.lsa_cache_attn(_host_cache(), Q, idx, cnt, stream=0)
 
 
 def test_append_cached_checks_before_the_call():
