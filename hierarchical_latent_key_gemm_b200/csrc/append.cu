@@ -70,7 +70,7 @@ struct CachedKeys {
             }
             const CT* p = static_cast<const CT*>(c.K) + cache_row(c, pid, h, tok) * a.d + k;
             if constexpr (sizeof(CT) == 1)
-                return e4m3x2_to_f32x2(*p).x * c.K_scale[(int64_t)pid * c.hkv + h];
+                return e4m3x4_to_f32x4(*p).x * c.K_scale[(int64_t)pid * c.hkv + h];
             else
                 return to_f32(*p);
         }, a.pool);

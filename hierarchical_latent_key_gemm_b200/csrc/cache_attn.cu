@@ -36,7 +36,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;                     // tokens of a warp's step
+constexpr int kStep = 32;                     // tokens of a warp's step: two tiles of 16
+constexpr int kStages = 3;                    // tiles of a warp's ring in shared memory
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kNoRow = 0xffffffffu;
 // Weights are at most 2^(kHeadroom + kLazy) and the largest at least 2^kHeadroom:
@@ -63,8 +64,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float value(const float* p) { return *p; }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -96,18 +101,59 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t*
     else mma_bf16(c, a, b[0], b[1]);
 }
 
+// Byte offset of 16-byte piece `i` of row r in a tile of rows of ROWB bytes:
+// permuted so that both the K pieces (8 rows, 4 neighbouring pieces) and the V
+// pieces (4 rows two apart, all pieces) of a warp's fragments hit 32 banks.
+template <int ROWB>
+__device__ __forceinline__ int piece_at(int r, int i) {
+    if constexpr (ROWB == 64) {
+        const int line = r >> 1;
+        return line * 128 + ((((r & 1) * 4 + i) ^ ((line & 3) << 1)) << 4);
+    } else {
+        const int s = ((r & 1) << 2) | ((r >> 1) & 3);
+        return r * ROWB + (((i & ~7) | ((i & 7) ^ s)) << 4);
+    }
+}
+
+// Place [i][g][2] of component d in the merge buffer: thread g's V pieces are
+// vp(g) (and vp(g) + 8 of rows of 16 pieces), m tile i its i-th two components.
+template <int ROWB, int BYTES>
+__device__ __forceinline__ int place(int d) {
+    const int byte = d * BYTES;
+    if constexpr (ROWB == 64) {       // 8 bytes a thread, in order
+        const int g = byte / 8;
+        return 16 * (byte % 8 / 2) + 2 * g + (d & 1);
+    } else {
+        const int piece = byte / 16 % 8, g = ((piece & 3) << 1) | (piece >> 2);
+        const int i = (byte / 128 * 16 + byte % 16) / (2 * BYTES);
+        return 16 * i + 2 * g + (d & 1);
+    }
+}
+
+// CTAs per SM that the registers are cut to
 template <int D, typename CT, typename T, int NT>
-__global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) {
+constexpr int min_ctas() {
+    if (sizeof(T) == 4) return 2;
+    if (NT == 2) return D == 64 ? 3 : 2;
+    return D * sizeof(CT) <= 128 ? 4 : 2;
+}
+
+template <int D, typename CT, typename T, int NT>
+__global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_attn_kernel(const AttnArgs a) {
     constexpr bool E4 = sizeof(CT) == 1;              // 8-bit codes, fp16 products; else bf16
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int PQ = F32 ? (E4 ? 2 : 3) : 1;        // 16-bit parts of a query component
     constexpr int PP = F32 ? (E4 ? 2 : 3) : (E4 ? 1 : 2);   // and of a weight
     constexpr int KS = D / 16;                        // k steps of K Q^T, m tiles of V^T P^T
     constexpr int HG = 8 * NT;                        // heads of a warp
-    constexpr int KW = D * (int)sizeof(CT) / 16;      // words of a K row in a thread (4 threads a row)
-    constexpr int VW = D * (int)sizeof(CT) / 32;      // words of a V row in a thread (8 threads a row)
+    constexpr int ROWB = D * (int)sizeof(CT);         // bytes of a row
+    constexpr int KW = ROWB / 16;                     // words of a K row in a thread (4 threads a row)
+    constexpr int VW = ROWB / 32;                     // words of a V row in a thread (8 threads a row)
+    constexpr int PIECES = ROWB / 16;
+    constexpr int TILE = 16 * ROWB;                   // bytes of 16 rows
     constexpr int LD = D + 4;                         // row stride of the merge buffer: no bank conflicts
-    __shared__ float acc_s[HG * LD];
+    extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][kStages][K tile, V tile]
+    float* acc_s = reinterpret_cast<float*>(ring_s);  // [HG][LD], once the rings are done with
     __shared__ float m_s[kWarps][HG], l_s[kWarps][HG];
     __shared__ float mc_s[HG], lc_s[HG];              // of the CTA
     __shared__ float f_s[kMaxCluster][HG], lt_s[HG], mt_s[HG];
@@ -116,20 +162,81 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int rank = blockIdx.x % a.cluster;
-    const int64_t unit = blockIdx.x / a.cluster;
-    const int grp = (int)(unit % a.groups);
-    const int64_t row = unit / a.groups;              // (b * nq + qi) * hkv + h
-    const int h = (int)(row % c.hkv);
-    const int64_t bq = row / c.hkv;
-    const int64_t b = bq / a.nq;
+    const uint32_t unit = blockIdx.x / a.cluster;
+    const int grp = unit % a.groups;
+    const uint32_t row = unit / a.groups;             // (b * nq + qi) * hkv + h
+    const int h = row % c.hkv;
+    const uint32_t bq = row / c.hkv;
+    const uint32_t b = bq / (uint32_t)a.nq;
     const int g0 = grp * HG, gn = min(HG, a.G - g0);
-    const int64_t q0 = (bq * a.hq + (int64_t)h * a.G + g0) * D;
+    const int64_t q0 = ((int64_t)bq * a.hq + h * a.G + g0) * D;
+
+    // ---- tokens: lane j looks up token j of the warp's step
     int n = a.cnt[row];
     if (n < 0 || n > a.max_sel) {
         if (tid == 0) latch(a.err, kErrDevice);
         n = n < 0 ? 0 : a.max_sel;
     }
-    const int32_t* ir = a.idx + row * a.max_sel;
+    const int32_t* ir = a.idx + (int64_t)row * a.max_sel;
+    const int32_t* table = c.table + (int64_t)b * c.ld_pages;
+    const int steps = (n + kStep - 1) / kStep;
+    const int stride = kWarps * a.cluster;
+    int step = rank * kWarps + warp;
+    struct Where {
+        uint32_t row;       // of the pools; kNoRow where there is no token
+        uint32_t ok;        // lanes that have one
+        float ks, vs;
+    };
+    auto fetch_token = [&](int st) -> int {
+        const int j = st * kStep + lane;
+        return j < n ? __ldg(ir + j) : -1;
+    };
+    auto look_up = [&](int st, int tok) -> Where {
+        Where w{kNoRow, 0u, 1.f, 1.f};
+        bool ok = false;
+        if (st * kStep + lane < n) {
+            const int col = tok >> c.log2_page;       // negative for a negative token
+            const int pid = (uint32_t)col < (uint32_t)c.ld_pages ? __ldg(table + col) : -1;
+            ok = (uint32_t)pid < (uint32_t)c.n_pages;
+            if (ok) {
+                const uint32_t ph = (uint32_t)pid * c.hkv + h;
+                w.row = (ph << c.log2_page) + (tok & (c.page - 1));
+                if (E4) {
+                    w.ks = __ldg(c.K_scale + ph);
+                    w.vs = __ldg(c.V_scale + ph);
+                }
+            } else {
+                latch(a.err, kErrDevice);
+            }
+        }
+        w.ok = __ballot_sync(0xffffffffu, ok);
+        return w;
+    };
+    Where cur = look_up(step, fetch_token(step));
+    int tok = fetch_token(step + stride);
+
+    // ---- gathered rows: 16 tokens' K and V rows to a stage of the warp's ring, 16 bytes a lane and copy; nothing is
+    // read, and zeros are written, where there is no token
+    unsigned char* ring = ring_s + warp * (kStages * 2 * TILE);
+    const uint32_t ring_u = smem_u32(ring);
+    const unsigned char* Kc = static_cast<const unsigned char*>(c.K) + 16 * (lane % PIECES);
+    const unsigned char* Vc = static_cast<const unsigned char*>(c.V) + 16 * (lane % PIECES);
+    auto gather = [&](uint32_t rows, int half, int stage) {
+#pragma unroll
+        for (int i = 0; i < PIECES / 2; ++i) {
+            const int r = i * (32 / PIECES) + lane / PIECES;
+            const uint32_t at = __shfl_sync(0xffffffffu, rows, 16 * half + r);
+            const int bytes = at != kNoRow ? 16 : 0;
+            const uint64_t off = at != kNoRow ? (uint64_t)at * ROWB : 0;
+            const uint32_t dst = ring_u + stage * 2 * TILE + piece_at<ROWB>(r, lane % PIECES);
+            cp_async16(dst, Kc + off, bytes);
+            cp_async16(dst + TILE, Vc + off, bytes);
+        }
+    };
+    if (step < steps) gather(cur.row, 0, 0);
+    cp_async_commit();
+    if (step < steps) gather(cur.row, 1, 1);
+    cp_async_commit();
 
     // ---- queries: B fragments, k slots in the order the K pieces come in
     uint32_t qf[PQ][KS][NT][2];
@@ -137,17 +244,15 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const T* q = static_cast<const T*>(a.Q) + q0 + (int64_t)(8 * nt + g) * D;
-        const bool live = 8 * nt + g < gn;
-        float v[KS][4];
+        float4 v[KS];
         float top = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int d0 = E4 ? 16 * (t + 4 * (s / 4)) + 4 * (s % 4) : 8 * (t + 4 * (s / 2)) + 4 * (s % 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[s][e] = live ? value(q + d0 + e) : 0.f;
-                top = fmaxf(top, fabsf(v[s][e]));
-            }
+            // the 4 components of k step s in this thread: one word of codes, two of bf16
+            const int w = E4 ? s : 2 * s;
+            const int d0 = (64 * (w / 4) + 16 * t + 4 * (w % 4)) / (int)sizeof(CT);
+            v[s] = 8 * nt + g < gn ? load4(q + d0) : make_float4(0.f, 0.f, 0.f, 0.f);
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(v[s].x), fabsf(v[s].y)), fmaxf(fabsf(v[s].z), fabsf(v[s].w))));
         }
         float up = 1.f, down = 1.f;
         if (E4) {
@@ -161,8 +266,8 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             uint32_t lo[PQ], hi[PQ];
-            split<E4, PQ>(v[s][0] * up, v[s][1] * up, lo);
-            split<E4, PQ>(v[s][2] * up, v[s][3] * up, hi);
+            split<E4, PQ>(v[s].x * up, v[s].y * up, lo);
+            split<E4, PQ>(v[s].z * up, v[s].w * up, hi);
 #pragma unroll
             for (int p = 0; p < PQ; ++p) {
                 qf[p][s][nt][0] = lo[p];
@@ -174,190 +279,184 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
     }
 
     float o[KS][NT][4];
+    // m: reference of a head's exponents, its largest so far less kHeadroom; unset: no score yet above -inf
     float m[NT][2], l[NT][2];
+    bool unset[NT][2], any_unset = true;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) { m[nt][e] = -INFINITY; l[nt][e] = 0.f; }
+        for (int e = 0; e < 2; ++e) { m[nt][e] = 0.f; l[nt][e] = 0.f; unset[nt][e] = true; }
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
     }
 
-    // ---- tokens: lane j (and j + 16) looks up token j of the warp's step
-    const int steps_all = (n + kTile - 1) / kTile;
-    const int stride = kWarps * a.cluster;
-    int step = rank * kWarps + warp;
-    auto fetch_token = [&](int st) -> int64_t {
-        const int j = st * kTile + (lane & 15);
-        return j < n ? (int64_t)__ldg(ir + j) : (int64_t)-1 - INT32_MAX - 1;   // below every int32: no token
-    };
-    constexpr int64_t kNoToken = (int64_t)-1 - INT32_MAX - 1;
-    struct Where { uint32_t row; float ks, vs; };
-    auto look_up = [&](int64_t tok) -> Where {
-        Where w{kNoRow, 1.f, 1.f};
-        if (tok == kNoToken) return w;
-        const int pid = cache_page(c, b, tok);
-        if (pid < 0) {
-            latch(a.err, kErrDevice);
-            return w;
-        }
-        w.row = (uint32_t)cache_row(c, pid, h, tok);
-        if (E4) {
-            w.ks = __ldg(c.K_scale + (int64_t)pid * c.hkv + h);
-            w.vs = __ldg(c.V_scale + (int64_t)pid * c.hkv + h);
-        }
-        return w;
-    };
-    const uint4* Kp = static_cast<const uint4*>(c.K);
-    const uint32_t* Vp = static_cast<const uint32_t*>(c.V);
-
-    int64_t tok = fetch_token(step);
-    Where cur = look_up(tok);
-    tok = fetch_token(step + stride);
-    for (; step < steps_all; step += stride) {
-        // K rows of tokens g and g + 8, V rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-        uint32_t kr[2][KW], vr[4][VW];
-        bool valid[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t r = __shfl_sync(0xffffffffu, cur.row, g + 8 * e);
-            valid[e] = r != kNoRow;
-#pragma unroll
-            for (int i = 0; i < KW / 4; ++i) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (valid[e]) v = __ldg(Kp + (int64_t)r * (KW) + t + 4 * i);
-                kr[e][4 * i] = v.x; kr[e][4 * i + 1] = v.y; kr[e][4 * i + 2] = v.z; kr[e][4 * i + 3] = v.w;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t r = __shfl_sync(0xffffffffu, cur.row, 2 * t + (e & 1) + 8 * (e >> 1));
-            const uint32_t* p = Vp + (int64_t)r * (8 * VW) + g * VW;
-            if constexpr (VW == 2) {
-                uint2 v = make_uint2(0, 0);
-                if (r != kNoRow) v = __ldg(reinterpret_cast<const uint2*>(p));
-                vr[e][0] = v.x; vr[e][1] = v.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < VW / 4; ++i) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r != kNoRow) v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-                    vr[e][4 * i] = v.x; vr[e][4 * i + 1] = v.y; vr[e][4 * i + 2] = v.z; vr[e][4 * i + 3] = v.w;
-                }
-            }
-        }
-        float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f}, iv[2] = {1.f, 1.f};
-        if (E4) {
-            const float lg = log2f(cur.vs), inv = __frcp_rn(cur.vs);   // both exact for powers of two
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ks[e] = __shfl_sync(0xffffffffu, cur.ks, g + 8 * e);
-                lv[e] = __shfl_sync(0xffffffffu, lg, g + 8 * e);
-                iv[e] = __shfl_sync(0xffffffffu, inv, g + 8 * e);
-            }
-        }
-        cur = look_up(tok);
+    const int vp = (g & 1) * (PIECES < 8 ? 0 : 4) + (g >> 1);   // this thread's V pieces, see piece_at
+    int stage = 0;
+    for (; step < steps; step += stride) {
+        const Where next = look_up(step + stride, tok);
         tok = fetch_token(step + 2 * stride);
-
-        // ---- scores: 16 tokens x 8 NT heads
-        float x[NT][4];
+        const int halves = n - step * kStep > 16 ? 2 : 1;
+        const float lg = E4 ? log2f(cur.vs) : 0.f, inv = E4 ? __frcp_rn(cur.vs) : 1.f;   // exact for powers of two
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int half = 0; half < 2; ++half) {
+            // the tile after the next one, into the stage that the last one left
+            const int free_stage = stage == 0 ? kStages - 1 : stage - 1;
+            if (step + stride < steps) gather(next.row, half, free_stage);
+            cp_async_commit();
+            if (half >= halves) break;
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const unsigned char* Ks = ring + stage * 2 * TILE;
+            const unsigned char* Vs = Ks + TILE;
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+            uint32_t kr[2][KW];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            uint32_t ka[4];
-            if constexpr (E4) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    ka[e] = e4m3x2_to_f16x2((uint16_t)kr[e][s]);
-                    ka[2 + e] = e4m3x2_to_f16x2((uint16_t)(kr[e][s] >> 16));
+                for (int i = 0; i < KW / 4; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(Ks + piece_at<ROWB>(g + 8 * e, t + 4 * i));
+                    kr[e][4 * i] = v.x; kr[e][4 * i + 1] = v.y; kr[e][4 * i + 2] = v.z; kr[e][4 * i + 3] = v.w;
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    ka[e] = kr[e][2 * s];
-                    ka[2 + e] = kr[e][2 * s + 1];
-                }
-            }
-#pragma unroll
-            for (int p = 0; p < PQ; ++p)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma<E4>(x[nt], ka, qf[p][s][nt]);
-        }
-        bool higher = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float y = fmaf(x[nt][e], ks[e >> 1] * qs[nt][e & 1], lv[e >> 1]);
-                x[nt][e] = valid[e >> 1] ? y : -INFINITY;
-                higher |= x[nt][e] > m[nt][e & 1] + kLazy;
-            }
-        if (__any_sync(0xffffffffu, higher)) {
+            // ---- scores: 16 tokens x 8 NT heads, even and odd k steps apart for shorter chains
+            float y[NT][4], z[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float top = fmaxf(x[nt][e], x[nt][e + 2]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    top = fmaxf(top, m[nt][e]);
-                    const float f = top == -INFINITY ? 1.f : ex2(m[nt][e] - top);
-                    m[nt][e] = top;
-                    l[nt][e] *= f;
+                for (int e = 0; e < 4; ++e) y[nt][e] = z[nt][e] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        o[i][nt][e] *= f;
-                        o[i][nt][e + 2] *= f;
+            for (int s = 0; s < KS; ++s) {
+                uint32_t ka[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (E4) {
+                        e4m3x4_to_f16x4(kr[e][s], ka[e], ka[2 + e]);
+                    } else {
+                        ka[e] = kr[e][2 * s];
+                        ka[2 + e] = kr[e][2 * s + 1];
                     }
                 }
-        }
-        // ---- weights: B fragments of P^T
-        uint32_t pb[PP][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
+                for (int p = 0; p < PQ; ++p)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma<E4>((s & 1) ? z[nt] : y[nt], ka, qf[p][s][nt]);
+            }
+
+            // ---- base-2 exponents of the weights
+            float iv[2] = {1.f, 1.f};
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float ks = 1.f, lv = 0.f;
+                if (E4) {
+                    ks = __shfl_sync(0xffffffffu, cur.ks, 16 * half + g + 8 * e);
+                    lv = __shfl_sync(0xffffffffu, lg, 16 * half + g + 8 * e);
+                    iv[e] = __shfl_sync(0xffffffffu, inv, 16 * half + g + 8 * e);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float& v = y[nt][2 * e + i];
+                        v = fmaf(v + z[nt][2 * e + i], ks * qs[nt][i], lv - m[nt][i]);
+                        top = fmaxf(top, v);
+                    }
+            }
+            const uint32_t have = cur.ok >> (16 * half) & 0xffffu;
+            if (have != 0xffffu) {     // past the row's end, or a token that was refused
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(have >> (g + 8 * (e >> 1)) & 1u)) y[nt][e] = -INFINITY;
+                top = INFINITY;        // maxima of what is left
+            }
+            if (__any_sync(0xffffffffu, top > kHeadroom + kLazy || any_unset)) {
+                // new references: 2^kHeadroom for the largest weight so far
+                any_unset = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float up = fmaxf(y[nt][e], y[nt][e + 2]);
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16)) - kHeadroom;
+                        const bool first = unset[nt][e];
+                        unset[nt][e] = first && up == -INFINITY;
+                        any_unset |= unset[nt][e];
+                        if (first ? up == -INFINITY : !(up > 0.f)) up = 0.f;
+                        const float f = first ? 1.f : ex2(-up);
+                        m[nt][e] += up;
+                        y[nt][e] -= up;
+                        y[nt][e + 2] -= up;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[i][nt][e] *= f;
+                            o[i][nt][e + 2] *= f;
+                        }
+                    }
+            }
+            // ---- weights: B fragments of P^T
+            uint32_t pb[PP][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = ex2(y[nt][e]);
+                    l[nt][e & 1] = fmaf(w[e], iv[e >> 1], l[nt][e & 1]);
+                }
+                uint32_t lo[PP], hi[PP];
+                split<E4, PP>(w[0], w[1], lo);
+                split<E4, PP>(w[2], w[3], hi);
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    pb[p][nt][0] = movmatrix_t(lo[p]);
+                    pb[p][nt][1] = movmatrix_t(hi[p]);
+                }
+            }
+            // ---- acc: rows g and g + 8 of m tile i are component(i, g) and the next
+            uint32_t vr[4][VW];        // rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float ref = m[nt][e & 1];
-                w[e] = ex2(x[nt][e] - (ref == -INFINITY ? 0.f : ref - kHeadroom));
-                l[nt][e & 1] = fmaf(w[e], iv[e >> 1], l[nt][e & 1]);
-            }
-            uint32_t lo[PP], hi[PP];
-            split<E4, PP>(w[0], w[1], lo);
-            split<E4, PP>(w[2], w[3], hi);
-#pragma unroll
-            for (int p = 0; p < PP; ++p) {
-                pb[p][nt][0] = movmatrix_t(lo[p]);
-                pb[p][nt][1] = movmatrix_t(hi[p]);
-            }
-        }
-        // ---- acc: rows g and g + 8 of m tile i are components (D/8) g + 2 i and the next
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            uint32_t va[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {       // tokens 2t, 2t + 1, then 2t + 8, 2t + 9
-                if constexpr (E4) {
-                    const uint32_t two = __byte_perm(vr[2 * e][i / 2], vr[2 * e + 1][i / 2], i % 2 ? 0x7362 : 0x5140);
-                    va[2 * e] = e4m3x2_to_f16x2((uint16_t)two);
-                    va[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(two >> 16));
+                const int r = 2 * t + (e & 1) + 8 * (e >> 1);
+                if constexpr (VW == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(Vs + piece_at<ROWB>(r, vp) + 8 * (g & 1));
+                    vr[e][0] = v.x; vr[e][1] = v.y;
                 } else {
-                    va[2 * e] = __byte_perm(vr[2 * e][i], vr[2 * e + 1][i], 0x5410);
-                    va[2 * e + 1] = __byte_perm(vr[2 * e][i], vr[2 * e + 1][i], 0x7632);
+#pragma unroll
+                    for (int i = 0; i < VW / 4; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(Vs + piece_at<ROWB>(r, vp + 8 * i));
+                        vr[e][4 * i] = v.x; vr[e][4 * i + 1] = v.y; vr[e][4 * i + 2] = v.z; vr[e][4 * i + 3] = v.w;
+                    }
                 }
             }
 #pragma unroll
-            for (int p = 0; p < PP; ++p)
+            for (int i = 0; i < KS; ++i) {
+                uint32_t va[4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma<E4>(o[i][nt], va, pb[p][nt]);
+                for (int e = 0; e < 2; ++e) {       // tokens 2t, 2t + 1, then 2t + 8, 2t + 9
+                    if constexpr (E4) {
+                        e4m3x4_to_f16x4(__byte_perm(vr[2 * e][i / 2], vr[2 * e + 1][i / 2], i % 2 ? 0x7362 : 0x5140),
+                                        va[2 * e], va[2 * e + 1]);
+                    } else {
+                        va[2 * e] = __byte_perm(vr[2 * e][i], vr[2 * e + 1][i], 0x5410);
+                        va[2 * e + 1] = __byte_perm(vr[2 * e][i], vr[2 * e + 1][i], 0x7632);
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma<E4>(o[i][nt], va, pb[p][nt]);
+            }
+            __syncwarp();
         }
+        cur = next;
     }
+    cp_async_wait<0>();
 
     // ---- merge the warps
 #pragma unroll
@@ -369,7 +468,7 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
             if (g == 0) {
-                m_s[warp][8 * nt + 2 * t + e] = m[nt][e];
+                m_s[warp][8 * nt + 2 * t + e] = unset[nt][e] ? -INFINITY : m[nt][e];
                 l_s[warp][8 * nt + 2 * t + e] = s;
             }
         }
@@ -384,10 +483,10 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
                     float M = m_s[0][head];
 #pragma unroll
                     for (int i = 1; i < kWarps; ++i) M = fmaxf(M, m_s[i][head]);
-                    const float f = M == -INFINITY ? 0.f : ex2(m[nt][e] - M);
+                    const float f = unset[nt][e] ? 0.f : ex2(m[nt][e] - M);
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
-                        // components (D/8) g + 2 i and the next, at the places [i][g]
+                        // component(i, g) and the next, at the places [i][g]
                         float2* p = reinterpret_cast<float2*>(acc_s + head * LD + 16 * i + 2 * g);
                         float2 s = make_float2(f * o[i][nt][e], f * o[i][nt][e + 2]);
                         if (w > 0) {
@@ -428,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
     __syncthreads();
     for (int e = rank * kThreads + tid; e < gn * D; e += a.cluster * kThreads) {
         const int head = e / D, d = e % D;
-        const int at = head * LD + 16 * ((d % (D / 8)) / 2) + 2 * (d / (D / 8)) + (d & 1);
+        const int at = head * LD + place<ROWB, (int)sizeof(CT)>(d);
         float s = 0.f;
         for (int i = 0; i < a.cluster; ++i) s += f_s[i][head] * cluster.map_shared_rank(acc_s, i)[at];
         const float L = lt_s[head];
@@ -436,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void cache_attn_kernel(const AttnArgs a) 
     }
     if (a.lse && rank == 0 && tid < gn) {
         const float L = lt_s[tid];
-        a.lse[q0 / D + tid] = L == 0.f ? -INFINITY : (mt_s[tid] - kHeadroom + log2f(L)) * 0.69314718055994531f;
+        a.lse[q0 / D + tid] = L == 0.f ? -INFINITY : (mt_s[tid] + log2f(L)) * 0.69314718055994531f;
     }
     if (a.cluster > 1) cluster.sync();
 }
@@ -445,14 +544,18 @@ template <int D, typename CT, typename T, int NT>
 int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     a.groups = (a.G + 8 * NT - 1) / (8 * NT);
     const int64_t units = rows * a.groups;
-    // few rows: a cluster of CTAs shares each, as long as its warps have two steps
-    const int steps = (a.max_sel + kTile - 1) / kTile;
+    // few rows: a cluster of CTAs shares each, as long as every warp has a step
+    const int steps = (a.max_sel + 31) / 32;
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && units * a.cluster < 2 * 148 && a.cluster * 2 * kWarps * 2 <= steps) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && units * a.cluster < 2 * 148 && a.cluster * 2 * kWarps <= steps) a.cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * a.cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
+    cfg.dynamicSmemBytes = (size_t)kWarps * kStages * 32 * D * sizeof(CT);
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CT, T, NT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = a.cluster;

@@ -39,15 +39,21 @@ __device__ __forceinline__ int64_t cache_row(const CacheArgs& c, int page_id, in
     return (((int64_t)page_id * c.hkv + h) << c.log2_page) + (tok & (c.page - 1));
 }
 
-// Two e4m3 codes (low byte first) to two fp16 values; exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
-    return r;
+// Four e4m3 codes (low byte first) to two pairs of fp16 values; exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{.reg .b16 l, h;\n"
+        "mov.b32 {l, h}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t v) {
-    const uint32_t h = e4m3x2_to_f16x2(v);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+__device__ __forceinline__ float4 e4m3x4_to_f32x4(uint32_t v) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16x4(v, lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 // Round to nearest even, saturating; NaN stays NaN.  lo lands in the low byte.
 __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {

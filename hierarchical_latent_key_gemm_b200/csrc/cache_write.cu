@@ -246,13 +246,8 @@ __global__ __launch_bounds__(kWriteThreads) void cache_write_kernel(const WriteA
                     const float ratio = old / s;
                     for (int e = 0; e < slot0 * D; e += 8) {
                         const uint2 w = *reinterpret_cast<const uint2*>(p + e);
-                        float v[8];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = e4m3x2_to_f32x2((uint16_t)((k < 2 ? w.x : w.y) >> (16 * (k & 1))));
-                            v[2 * k] = f.x;
-                            v[2 * k + 1] = f.y;
-                        }
+                        const float4 f0 = e4m3x4_to_f32x4(w.x), f1 = e4m3x4_to_f32x4(w.y);
+                        const float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
                         store8(p + e, v, ratio);
                     }
                 } else {

@@ -470,6 +470,10 @@ def test_attention_refuses_what_it_cannot_take():
         lsa.lsa_cache_attn(c, flat[1:65].view(1, 1, 1, 64), idx, cnt)
     with pytest.raises(ValueError, match="contiguous"):
         lsa.lsa_cache_attn(c, torch.zeros(1, 1, 2, 128, dtype=BF, device="cuda")[..., ::2], idx, cnt)
+    pool = torch.zeros(4 * 16 * 64 + 32, dtype=E4, device="cuda")[8:-24].view(4, 1, 16, 64)
+    odd = lsa.KVCache(pool, pool.clone(), c.page_table, c.K_scale[:4].contiguous(), c.V_scale[:4].contiguous())
+    with pytest.raises(lsa.LsaError):           # pools not on a 16-byte boundary
+        lsa.lsa_cache_attn(odd, torch.zeros(1, 1, 4, 64, dtype=BF, device="cuda"), idx, cnt)
     none = torch.zeros(1, 0, 4, 64, dtype=BF, device="cuda")
     Oo, lse = lsa.lsa_cache_attn(c, none, idx[:, :0], cnt[:, :0])
     assert Oo.shape == none.shape and lse.shape == (1, 0, 4)
