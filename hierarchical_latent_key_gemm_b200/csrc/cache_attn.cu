@@ -36,10 +36,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 32;                     // tokens of a warp's step: two tiles of 16
-constexpr int kStages = 3;                    // tiles of a warp's ring in shared memory
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kNoRow = 0xffffffffu;
 // Weights are at most 2^(kHeadroom + kLazy) and the largest at least 2^kHeadroom:
 // the maximum is renewed only when a score passes it by 2^kLazy.  In fp16 a
 // weight keeps 11 bits down to 2^-(14 + kHeadroom) of the largest, and what lies
@@ -63,6 +60,13 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// log2 of a positive normal number, exact for powers of two
+__device__ __forceinline__ float log2_of(float x) {
+    float y;
+    const int bits = __float_as_int(x);
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__int_as_float((bits & 0x7fffff) | 0x3f800000)));
+    return (float)((bits >> 23) - 127) + y;
 }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -95,6 +99,23 @@ __device__ __forceinline__ void split(float a, float b, uint32_t* p) {
     }
 }
 
+// c = a b, the first product of a chain
+template <bool F16>
+__device__ __forceinline__ void mma_first(float* c, const uint32_t* a, const uint32_t* b) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};\n"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};\n"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t* b) {
     if constexpr (F16) mma_f16(c, a, b[0], b[1]);
@@ -113,6 +134,23 @@ __device__ __forceinline__ int piece_at(int r, int i) {
         const int s = ((r & 1) << 2) | ((r >> 1) & 3);
         return r * ROWB + (((i & ~7) | ((i & 7) ^ s)) << 4);
     }
+}
+
+template <int N>
+__device__ __forceinline__ void load_shared(uint32_t p, uint32_t* w) {
+    if constexpr (N == 2)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p) : "memory");
+    else
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(p)
+                     : "memory");
+}
+
+// piece_at(i * 32 / PIECES + r, p) = (piece_at(r, p) ^ step_swizzle(i)) + i * (32 / PIECES) * ROWB
+template <int ROWB>
+__device__ __forceinline__ constexpr uint32_t step_swizzle(int i) {
+    return ROWB == 64 ? 0u : ROWB == 128 ? (i & 1) << 5 : (i & 3) << 4;
 }
 
 // Place [i][g][2] of component d in the merge buffer: thread g's V pieces are
@@ -134,9 +172,13 @@ __device__ __forceinline__ int place(int d) {
 template <int D, typename CT, typename T, int NT>
 constexpr int min_ctas() {
     if (sizeof(T) == 4) return 2;
-    if (NT == 2) return D == 64 ? 3 : 2;
-    return D * sizeof(CT) <= 128 ? 4 : 2;
+    return NT == 2 ? (D == 64 ? 3 : 2) : (D * sizeof(CT) == 64 ? 4 : 3);
 }
+
+// Tiles of 16 tokens of a warp's step.  Two steps are in shared memory: 8 KB of
+// rows each (4 KB of 64-byte rows).
+template <int D, typename CT>
+constexpr int tiles_per_step() { return D * sizeof(CT) <= 128 ? 2 : 1; }
 
 template <int D, typename CT, typename T, int NT>
 __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_attn_kernel(const AttnArgs a) {
@@ -151,8 +193,11 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     constexpr int VW = ROWB / 32;                     // words of a V row in a thread (8 threads a row)
     constexpr int PIECES = ROWB / 16;
     constexpr int TILE = 16 * ROWB;                   // bytes of 16 rows
+    constexpr int TPS = tiles_per_step<D, CT>();
+    constexpr int STEP = 16 * TPS;                    // tokens of a warp's step
+    constexpr int BUFFER = TPS * 2 * TILE;            // bytes of a step: (K tile, V tile) TPS times
     constexpr int LD = D + 4;                         // row stride of the merge buffer: no bank conflicts
-    extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][kStages][K tile, V tile]
+    extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][2][BUFFER]
     float* acc_s = reinterpret_cast<float*>(ring_s);  // [HG][LD], once the rings are done with
     __shared__ float m_s[kWarps][HG], l_s[kWarps][HG];
     __shared__ float mc_s[HG], lc_s[HG];              // of the CTA
@@ -179,64 +224,82 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     }
     const int32_t* ir = a.idx + (int64_t)row * a.max_sel;
     const int32_t* table = c.table + (int64_t)b * c.ld_pages;
-    const int steps = (n + kStep - 1) / kStep;
+    const int steps = (n + STEP - 1) / STEP;
     const int stride = kWarps * a.cluster;
     int step = rank * kWarps + warp;
+    // Three loads follow one another for a row: the token, its page, the row and
+    // its scales.  They are taken one step apart, so that none is waited for:
+    // tokens are fetched three steps ahead, pages two, rows and scales one.
     struct Where {
-        uint32_t row;       // of the pools; kNoRow where there is no token
+        uint32_t row;       // of the pools; 0 where there is no token
         uint32_t ok;        // lanes that have one
         float ks, vs;
     };
-    auto fetch_token = [&](int st) -> int {
-        const int j = st * kStep + lane;
-        return j < n ? __ldg(ir + j) : -1;
+    auto fetch_token = [&](int st) -> int {           // -1 past the row's end
+        const int j = st * STEP + lane;
+        return (STEP == 32 || lane < STEP) && j < n ? __ldg(ir + j) : -1;
     };
-    auto look_up = [&](int st, int tok) -> Where {
-        Where w{kNoRow, 0u, 1.f, 1.f};
-        bool ok = false;
-        if (st * kStep + lane < n) {
-            const int col = tok >> c.log2_page;       // negative for a negative token
-            const int pid = (uint32_t)col < (uint32_t)c.ld_pages ? __ldg(table + col) : -1;
-            ok = (uint32_t)pid < (uint32_t)c.n_pages;
-            if (ok) {
-                const uint32_t ph = (uint32_t)pid * c.hkv + h;
-                w.row = (ph << c.log2_page) + (tok & (c.page - 1));
-                if (E4) {
-                    w.ks = __ldg(c.K_scale + ph);
-                    w.vs = __ldg(c.V_scale + ph);
-                }
-            } else {
-                latch(a.err, kErrDevice);
-            }
-        }
+    auto fetch_page = [&](int tok) -> int {
+        const int col = tok >> c.log2_page;           // negative for a negative token
+        return (uint32_t)col < (uint32_t)c.ld_pages ? __ldg(table + col) : -1;
+    };
+    auto locate = [&](int st, int tok, int pid) -> Where {
+        Where w{0u, 0u, 1.f, 1.f};
+        const bool ok = (uint32_t)pid < (uint32_t)c.n_pages;
         w.ok = __ballot_sync(0xffffffffu, ok);
+        if (ok) {
+            const uint32_t ph = (uint32_t)pid * c.hkv + h;
+            w.row = (ph << c.log2_page) + (tok & (c.page - 1));
+            if (E4) {
+                w.ks = __ldg(c.K_scale + ph);
+                w.vs = __ldg(c.V_scale + ph);
+            }
+        } else if ((STEP == 32 || lane < STEP) && st * STEP + lane < n) {
+            latch(a.err, kErrDevice);
+        }
         return w;
     };
-    Where cur = look_up(step, fetch_token(step));
-    int tok = fetch_token(step + stride);
 
-    // ---- gathered rows: 16 tokens' K and V rows to a stage of the warp's ring, 16 bytes a lane and copy; nothing is
-    // read, and zeros are written, where there is no token
-    unsigned char* ring = ring_s + warp * (kStages * 2 * TILE);
-    const uint32_t ring_u = smem_u32(ring);
+    // ---- gathered rows: a step's K and V rows to the warp's shared memory, 16
+    // bytes a lane and copy; zeros where there is no token
+    const uint32_t ring = smem_u32(ring_s) + warp * 2 * BUFFER;
     const unsigned char* Kc = static_cast<const unsigned char*>(c.K) + 16 * (lane % PIECES);
-    const unsigned char* Vc = static_cast<const unsigned char*>(c.V) + 16 * (lane % PIECES);
-    auto gather = [&](uint32_t rows, int half, int stage) {
+    const int64_t k_to_v = static_cast<const unsigned char*>(c.V) - static_cast<const unsigned char*>(c.K);
+    const uint32_t lane_at = piece_at<ROWB>(lane / PIECES, lane % PIECES);
+    auto gather = [&](const Where& w, int half, uint32_t buffer) {
+        constexpr int RP = 32 / PIECES;               // rows of a copy
+        if ((w.ok >> (16 * half) & 0xffffu) == 0xffffu) {
 #pragma unroll
-        for (int i = 0; i < PIECES / 2; ++i) {
-            const int r = i * (32 / PIECES) + lane / PIECES;
-            const uint32_t at = __shfl_sync(0xffffffffu, rows, 16 * half + r);
-            const int bytes = at != kNoRow ? 16 : 0;
-            const uint64_t off = at != kNoRow ? (uint64_t)at * ROWB : 0;
-            const uint32_t dst = ring_u + stage * 2 * TILE + piece_at<ROWB>(r, lane % PIECES);
-            cp_async16(dst, Kc + off, bytes);
-            cp_async16(dst + TILE, Vc + off, bytes);
+            for (int i = 0; i < 16 / RP; ++i) {
+                const uint32_t at = __shfl_sync(0xffffffffu, w.row, 16 * half + i * RP + lane / PIECES);
+                const unsigned char* src = Kc + (uint64_t)at * ROWB;
+                const uint32_t dst = buffer + (lane_at ^ step_swizzle<ROWB>(i)) + (half * 2 * TILE + i * RP * ROWB);
+                cp_async16(dst, src);
+                cp_async16(dst + TILE, src + k_to_v);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16 / RP; ++i) {
+                const int j = 16 * half + i * RP + lane / PIECES;
+                const uint32_t at = __shfl_sync(0xffffffffu, w.row, j);
+                const unsigned char* src = Kc + (uint64_t)at * ROWB;
+                const uint32_t dst = buffer + (lane_at ^ step_swizzle<ROWB>(i)) + (half * 2 * TILE + i * RP * ROWB);
+                const int bytes = w.ok >> j & 1u ? 16 : 0;
+                cp_async16(dst, src, bytes);
+                cp_async16(dst + TILE, src + k_to_v, bytes);
+            }
         }
     };
-    if (step < steps) gather(cur.row, 0, 0);
-    cp_async_commit();
-    if (step < steps) gather(cur.row, 1, 1);
-    cp_async_commit();
+    int tok = fetch_token(step);
+    Where cur = locate(step, tok, fetch_page(tok));
+#pragma unroll
+    for (int half = 0; half < TPS; ++half) {
+        if (step < steps) gather(cur, half, ring);
+        cp_async_commit();
+    }
+    tok = fetch_token(step + stride);
+    int pid = fetch_page(tok);
+    int tok2 = fetch_token(step + 2 * stride);
 
     // ---- queries: B fragments, k slots in the order the K pieces come in
     uint32_t qf[PQ][KS][NT][2];
@@ -292,39 +355,44 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
     }
 
-    const int vp = (g & 1) * (PIECES < 8 ? 0 : 4) + (g >> 1);   // this thread's V pieces, see piece_at
-    int stage = 0;
+    // shared addresses of this thread's pieces: K pieces t + 4 i of rows g + 8 e, V pieces vp + 8 i of rows
+    // 2t + (e & 1) + 8 (e >> 1)
+    const int vp = (g & 1) * (PIECES < 8 ? 0 : 4) + (g >> 1);
+    uint32_t k0 = ring + piece_at<ROWB>(g, t), k1 = ring + piece_at<ROWB>(g, t + (PIECES < 8 ? 0 : 4));
+    uint32_t v0 = ring + piece_at<ROWB>(2 * t, vp) + (VW == 2 ? 8 * (g & 1) : 0);
+    uint32_t v1 = ring + piece_at<ROWB>(2 * t + 1, vp) + (VW == 2 ? 8 * (g & 1) : 0);
+    uint32_t ahead = ring + BUFFER;
+    int32_t flip = BUFFER;
     for (; step < steps; step += stride) {
-        const Where next = look_up(step + stride, tok);
-        tok = fetch_token(step + 2 * stride);
-        const int halves = n - step * kStep > 16 ? 2 : 1;
-        const float lg = E4 ? log2f(cur.vs) : 0.f, inv = E4 ? __frcp_rn(cur.vs) : 1.f;   // exact for powers of two
+        // the next step's rows into the buffer that the last one left
+        const Where next = locate(step + stride, tok, pid);
+        tok = tok2;
+        pid = fetch_page(tok);
+        tok2 = fetch_token(step + 3 * stride);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // the tile after the next one, into the stage that the last one left
-            const int free_stage = stage == 0 ? kStages - 1 : stage - 1;
-            if (step + stride < steps) gather(next.row, half, free_stage);
+        for (int half = 0; half < TPS; ++half) {
+            if (step + stride < steps) gather(next, half, ahead);
             cp_async_commit();
-            if (half >= halves) break;
-            cp_async_wait<kStages - 1>();
+        }
+        const float lg = E4 ? log2_of(cur.vs) : 0.f, inv = E4 ? ex2(-lg) : 1.f;
+#pragma unroll
+        for (int half = 0; half < TPS; ++half) {
+            if (half == 0) {
+                cp_async_wait<2 * TPS - 1>();
+            } else {
+                if (n - step * STEP <= 16) break;
+                cp_async_wait<2>();
+            }
             __syncwarp();
-            const unsigned char* Ks = ring + stage * 2 * TILE;
-            const unsigned char* Vs = Ks + TILE;
-            stage = stage == kStages - 1 ? 0 : stage + 1;
             uint32_t kr[2][KW];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int i = 0; i < KW / 4; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(Ks + piece_at<ROWB>(g + 8 * e, t + 4 * i));
-                    kr[e][4 * i] = v.x; kr[e][4 * i + 1] = v.y; kr[e][4 * i + 2] = v.z; kr[e][4 * i + 3] = v.w;
-                }
+                for (int i = 0; i < KW / 4; ++i)
+                    load_shared<4>((i & 1 ? k1 : k0) + (half * 2 * TILE + 8 * e * ROWB + 128 * (i / 2)),
+                                   kr[e] + 4 * i);
             // ---- scores: 16 tokens x 8 NT heads, even and odd k steps apart for shorter chains
             float y[NT][4], z[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[nt][e] = z[nt][e] = 0.f;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 uint32_t ka[4];
@@ -340,7 +408,11 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
 #pragma unroll
                 for (int p = 0; p < PQ; ++p)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma<E4>((s & 1) ? z[nt] : y[nt], ka, qf[p][s][nt]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float* acc = (s & 1) ? z[nt] : y[nt];
+                        if (s < 2 && p == 0) mma_first<E4>(acc, ka, qf[p][s][nt]);
+                        else mma<E4>(acc, ka, qf[p][s][nt]);
+                    }
             }
 
             // ---- base-2 exponents of the weights
@@ -422,16 +494,12 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             uint32_t vr[4][VW];        // rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int r = 2 * t + (e & 1) + 8 * (e >> 1);
+                const uint32_t p = (e & 1 ? v1 : v0) + (half * 2 * TILE + TILE + 8 * (e >> 1) * ROWB);
                 if constexpr (VW == 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(Vs + piece_at<ROWB>(r, vp) + 8 * (g & 1));
-                    vr[e][0] = v.x; vr[e][1] = v.y;
+                    load_shared<2>(p, vr[e]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < VW / 4; ++i) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(Vs + piece_at<ROWB>(r, vp + 8 * i));
-                        vr[e][4 * i] = v.x; vr[e][4 * i + 1] = v.y; vr[e][4 * i + 2] = v.z; vr[e][4 * i + 3] = v.w;
-                    }
+                    for (int i = 0; i < VW / 4; ++i) load_shared<4>(p + 128 * i, vr[e] + 4 * i);
                 }
             }
 #pragma unroll
@@ -452,9 +520,15 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma<E4>(o[i][nt], va, pb[p][nt]);
             }
-            __syncwarp();
         }
+        __syncwarp();          // the buffer is free
         cur = next;
+        ahead -= flip;
+        k0 += flip;
+        k1 += flip;
+        v0 += flip;
+        v1 += flip;
+        flip = -flip;
     }
     cp_async_wait<0>();
 
@@ -552,7 +626,7 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(units * a.cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cfg.dynamicSmemBytes = (size_t)kWarps * kStages * 32 * D * sizeof(CT);
+    cfg.dynamicSmemBytes = (size_t)kWarps * 2 * tiles_per_step<D, CT>() * 32 * D * sizeof(CT);
     const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CT, T, NT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return cuda_status(e);
