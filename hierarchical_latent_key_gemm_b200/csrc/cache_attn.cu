@@ -375,15 +375,12 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             cp_async_commit();
         }
         const float lg = E4 ? log2_of(cur.vs) : 0.f, inv = E4 ? ex2(-lg) : 1.f;
+        cp_async_wait<TPS>();
+        __syncwarp();
+        // ---- scores: STEP tokens x 8 NT heads, even and odd k steps apart for shorter chains
+        float y[TPS][NT][4];
 #pragma unroll
         for (int half = 0; half < TPS; ++half) {
-            if (half == 0) {
-                cp_async_wait<2 * TPS - 1>();
-            } else {
-                if (n - step * STEP <= 16) break;
-                cp_async_wait<2>();
-            }
-            __syncwarp();
             uint32_t kr[2][KW];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -391,8 +388,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 for (int i = 0; i < KW / 4; ++i)
                     load_shared<4>((i & 1 ? k1 : k0) + (half * 2 * TILE + 8 * e * ROWB + 128 * (i / 2)),
                                    kr[e] + 4 * i);
-            // ---- scores: 16 tokens x 8 NT heads, even and odd k steps apart for shorter chains
-            float y[NT][4], z[NT][4];
+            float z[NT][4];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 uint32_t ka[4];
@@ -409,88 +405,85 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 for (int p = 0; p < PQ; ++p)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float* acc = (s & 1) ? z[nt] : y[nt];
+                        float* acc = (s & 1) ? z[nt] : y[half][nt];
                         if (s < 2 && p == 0) mma_first<E4>(acc, ka, qf[p][s][nt]);
                         else mma<E4>(acc, ka, qf[p][s][nt]);
                     }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[half][nt][e] += z[nt][e];
+        }
 
-            // ---- base-2 exponents of the weights
-            float iv[2] = {1.f, 1.f};
-            float top = -INFINITY;
+        // ---- base-2 exponents of the weights
+        float iv[TPS][2];
+        float top = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < TPS; ++half)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float ks = 1.f, lv = 0.f;
+                iv[half][e] = 1.f;
                 if (E4) {
                     ks = __shfl_sync(0xffffffffu, cur.ks, 16 * half + g + 8 * e);
                     lv = __shfl_sync(0xffffffffu, lg, 16 * half + g + 8 * e);
-                    iv[e] = __shfl_sync(0xffffffffu, inv, 16 * half + g + 8 * e);
+                    iv[half][e] = __shfl_sync(0xffffffffu, inv, 16 * half + g + 8 * e);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float& v = y[nt][2 * e + i];
-                        v = fmaf(v + z[nt][2 * e + i], ks * qs[nt][i], lv - m[nt][i]);
+                        float& v = y[half][nt][2 * e + i];
+                        v = fmaf(v, ks * qs[nt][i], lv - m[nt][i]);
                         top = fmaxf(top, v);
                     }
             }
-            const uint32_t have = cur.ok >> (16 * half) & 0xffffu;
-            if (have != 0xffffu) {     // past the row's end, or a token that was refused
+        constexpr uint32_t kFull = STEP == 32 ? 0xffffffffu : 0xffffu;
+        if (cur.ok != kFull) {         // past the row's end, or a token that was refused
+#pragma unroll
+            for (int half = 0; half < TPS; ++half)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!(have >> (g + 8 * (e >> 1)) & 1u)) y[nt][e] = -INFINITY;
-                top = INFINITY;        // maxima of what is left
-            }
-            if (__any_sync(0xffffffffu, top > kHeadroom + kLazy || any_unset)) {
-                // new references: 2^kHeadroom for the largest weight so far
-                any_unset = false;
+                        if (!(cur.ok >> (16 * half + g + 8 * (e >> 1)) & 1u)) y[half][nt][e] = -INFINITY;
+            top = INFINITY;            // maxima of what is left
+        }
+        if (__any_sync(0xffffffffu, top > kHeadroom + kLazy || any_unset)) {
+            // new references: 2^kHeadroom for the largest weight so far
+            any_unset = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float up = fmaxf(y[nt][e], y[nt][e + 2]);
-                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
-                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
-                        up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16)) - kHeadroom;
-                        const bool first = unset[nt][e];
-                        unset[nt][e] = first && up == -INFINITY;
-                        any_unset |= unset[nt][e];
-                        if (first ? up == -INFINITY : !(up > 0.f)) up = 0.f;
-                        const float f = first ? 1.f : ex2(-up);
-                        m[nt][e] += up;
-                        y[nt][e] -= up;
-                        y[nt][e + 2] -= up;
-                        l[nt][e] *= f;
+                for (int e = 0; e < 2; ++e) {
+                    float up = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < KS; ++i) {
-                            o[i][nt][e] *= f;
-                            o[i][nt][e + 2] *= f;
-                        }
+                    for (int half = 0; half < TPS; ++half) up = fmaxf(up, fmaxf(y[half][nt][e], y[half][nt][e + 2]));
+                    up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+                    up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+                    up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16)) - kHeadroom;
+                    const bool first = unset[nt][e];
+                    unset[nt][e] = first && up == -INFINITY;
+                    any_unset |= unset[nt][e];
+                    if (first ? up == -INFINITY : !(up > 0.f)) up = 0.f;
+                    const float f = first ? 1.f : ex2(-up);
+                    m[nt][e] += up;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int half = 0; half < TPS; ++half) {
+                        y[half][nt][e] -= up;
+                        y[half][nt][e + 2] -= up;
                     }
-            }
-            // ---- weights: B fragments of P^T
-            uint32_t pb[PP][NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = ex2(y[nt][e]);
-                    l[nt][e & 1] = fmaf(w[e], iv[e >> 1], l[nt][e & 1]);
+                    for (int i = 0; i < KS; ++i) {
+                        o[i][nt][e] *= f;
+                        o[i][nt][e + 2] *= f;
+                    }
                 }
-                uint32_t lo[PP], hi[PP];
-                split<E4, PP>(w[0], w[1], lo);
-                split<E4, PP>(w[2], w[3], hi);
+        }
 #pragma unroll
-                for (int p = 0; p < PP; ++p) {
-                    pb[p][nt][0] = movmatrix_t(lo[p]);
-                    pb[p][nt][1] = movmatrix_t(hi[p]);
-                }
-            }
-            // ---- acc: rows g and g + 8 of m tile i are component(i, g) and the next
+        for (int half = 0; half < TPS; ++half) {
             uint32_t vr[4][VW];        // rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -502,6 +495,26 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     for (int i = 0; i < VW / 4; ++i) load_shared<4>(p + 128 * i, vr[e] + 4 * i);
                 }
             }
+            // ---- weights: B fragments of P^T
+            uint32_t pb[PP][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = ex2(y[half][nt][e]);
+                    l[nt][e & 1] = fmaf(w[e], iv[half][e >> 1], l[nt][e & 1]);
+                }
+                uint32_t lo[PP], hi[PP];
+                split<E4, PP>(w[0], w[1], lo);
+                split<E4, PP>(w[2], w[3], hi);
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    pb[p][nt][0] = movmatrix_t(lo[p]);
+                    pb[p][nt][1] = movmatrix_t(hi[p]);
+                }
+            }
+            // ---- acc: rows g and g + 8 of m tile i are component(i, g) and the next
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 uint32_t va[4];
