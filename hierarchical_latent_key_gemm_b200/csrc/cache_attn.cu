@@ -19,12 +19,10 @@
 // them, without shared memory.  8-bit codes become fp16 exactly; queries are
 // scaled by a power of two per head so that bf16 values are fp16 values too.
 //
-// The warps of a CTA, and the CTAs of a cluster, take every n-th 16 tokens of
-// one row; their (m, l, acc) are merged in shared and distributed shared
-// memory in a fixed order.
+// The warps of a CTA, and the CTAs of a cluster, take every n-th step of one
+// row; their (m, l, acc) are merged in shared and distributed shared memory in
+// a fixed order.
 #include <cooperative_groups.h>
-
-#include <algorithm>
 
 #include "cache_common.cuh"
 #include "warp_mma.cuh"
@@ -51,7 +49,9 @@ struct AttnArgs {
     void* O;
     float* lse;
     int64_t nq;
-    int hq, G, max_sel, groups, cluster;
+    int hq, G, max_sel, groups;
+    uint32_t units;        // (row, group of heads)
+    int warps, cluster;    // warps of a CTA that share a unit (1 or kWarps), CTAs that do
     float scale_log2;
     int32_t* err;
 };
@@ -74,8 +74,6 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                        __uint_as_float(v.y & 0xffff0000u));
 }
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // Two floats as `N` pairs of 16-bit floats whose sums carry them: fp16 parts
 // (11 bits each) next to 8-bit codes, bf16 parts (8 bits each) next to bf16.
@@ -153,19 +151,22 @@ __device__ __forceinline__ constexpr uint32_t step_swizzle(int i) {
     return ROWB == 64 ? 0u : ROWB == 128 ? (i & 1) << 5 : (i & 3) << 4;
 }
 
-// Place [i][g][2] of component d in the merge buffer: thread g's V pieces are
-// vp(g) (and vp(g) + 8 of rows of 16 pieces), m tile i its i-th two components.
-template <int ROWB, int BYTES>
-__device__ __forceinline__ int place(int d) {
-    const int byte = d * BYTES;
-    if constexpr (ROWB == 64) {       // 8 bytes a thread, in order
-        const int g = byte / 8;
-        return 16 * (byte % 8 / 2) + 2 * g + (d & 1);
-    } else {
-        const int piece = byte / 16 % 8, g = ((piece & 3) << 1) | (piece >> 2);
-        const int i = (byte / 128 * 16 + byte % 16) / (2 * BYTES);
-        return 16 * i + 2 * g + (d & 1);
-    }
+// Which pair of components m tile i of thread g is: its V pieces are vp(g) (and
+// vp(g) + 8 of rows of 16 pieces), 8 bytes each of rows of 4 pieces.
+template <int D, int BYTES>
+__device__ __forceinline__ int pair_of(int i, int g) {
+    if constexpr (D * BYTES == 64) return 4 * g + i;
+    const int vp = (g & 1) * 4 + (g >> 1);
+    if constexpr (BYTES == 1) return 8 * vp + i;
+    return (i / 4) * 32 + 4 * vp + (i & 3);
+}
+// Where pair q of a head stands in the merge buffer: permuted so that neither
+// the fragments' writes nor the reads in order meet in a bank (two writes do).
+__device__ __forceinline__ int pair_at(int q) { return 2 * ((q & ~7) | ((q ^ (q >> 3)) & 7)); }
+
+__device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
 }
 
 // CTAs per SM that the registers are cut to
@@ -196,18 +197,21 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     constexpr int TPS = tiles_per_step<D, CT>();
     constexpr int STEP = 16 * TPS;                    // tokens of a warp's step
     constexpr int BUFFER = TPS * 2 * TILE;            // bytes of a step: (K tile, V tile) TPS times
-    constexpr int LD = D + 4;                         // row stride of the merge buffer: no bank conflicts
-    extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][2][BUFFER]
-    float* acc_s = reinterpret_cast<float*>(ring_s);  // [HG][LD], once the rings are done with
+    constexpr int LD = D + 2;                         // row stride of the merge buffers
+    extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][2][BUFFER]; at the end [HG][LD] of a warp
     __shared__ float m_s[kWarps][HG], l_s[kWarps][HG];
-    __shared__ float mc_s[HG], lc_s[HG];              // of the CTA
-    __shared__ float f_s[kMaxCluster][HG], lt_s[HG], mt_s[HG];
+    // what the CTAs of a cluster send: a share of the sums, and all maxima and sums of weights
+    __shared__ float2 sum_r[HG * D / 2];
+    __shared__ float m_r[kMaxCluster][HG], l_r[kMaxCluster][HG];
 
     const CacheArgs& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int rank = blockIdx.x % a.cluster;
-    const uint32_t unit = blockIdx.x / a.cluster;
+    if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // all have started: waited for below
+    const bool alone = a.warps == 1;                  // a warp takes a whole row
+    const uint32_t unit = alone ? blockIdx.x * kWarps + warp : blockIdx.x / a.cluster;
+    if (unit >= a.units) return;                      // only in the last CTA of whole-row warps
     const int grp = unit % a.groups;
     const uint32_t row = unit / a.groups;             // (b * nq + qi) * hkv + h
     const int h = row % c.hkv;
@@ -217,16 +221,35 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     const int64_t q0 = ((int64_t)bq * a.hq + h * a.G + g0) * D;
 
     // ---- tokens: lane j looks up token j of the warp's step
-    int n = a.cnt[row];
+    const int32_t* ir = a.idx + (int64_t)row * a.max_sel;
+    const int32_t* table = c.table + (int64_t)b * c.ld_pages;
+    const int stride = alone ? 1 : kWarps * a.cluster;
+    int step = alone ? 0 : rank * kWarps + warp;
+    // the first tokens are read with the row's length, not after it
+    auto fetch_token = [&](int st, int end) -> int {  // -1 past the row's end
+        const int j = st * STEP + lane;
+        return (STEP == 32 || lane < STEP) && j < end ? __ldg(ir + j) : -1;
+    };
+    int n = __ldg(a.cnt + row);
+    int tok = fetch_token(step, a.max_sel), tok1 = fetch_token(step + stride, a.max_sel);
+    // and the queries before anything waits
+    float4 qv[NT][KS];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const T* q = static_cast<const T*>(a.Q) + q0 + (int64_t)(8 * nt + g) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            // the 4 components of k step s in this thread: one word of codes, two of bf16
+            const int w = E4 ? s : 2 * s;
+            const int d0 = (64 * (w / 4) + 16 * t + 4 * (w % 4)) / (int)sizeof(CT);
+            qv[nt][s] = 8 * nt + g < gn ? load4(q + d0) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
     if (n < 0 || n > a.max_sel) {
         if (tid == 0) latch(a.err, kErrDevice);
         n = n < 0 ? 0 : a.max_sel;
     }
-    const int32_t* ir = a.idx + (int64_t)row * a.max_sel;
-    const int32_t* table = c.table + (int64_t)b * c.ld_pages;
     const int steps = (n + STEP - 1) / STEP;
-    const int stride = kWarps * a.cluster;
-    int step = rank * kWarps + warp;
     // Three loads follow one another for a row: the token, its page, the row and
     // its scales.  They are taken one step apart, so that none is waited for:
     // tokens are fetched three steps ahead, pages two, rows and scales one.
@@ -235,17 +258,14 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
         uint32_t ok;        // lanes that have one
         float ks, vs;
     };
-    auto fetch_token = [&](int st) -> int {           // -1 past the row's end
-        const int j = st * STEP + lane;
-        return (STEP == 32 || lane < STEP) && j < n ? __ldg(ir + j) : -1;
-    };
     auto fetch_page = [&](int tok) -> int {
         const int col = tok >> c.log2_page;           // negative for a negative token
         return (uint32_t)col < (uint32_t)c.ld_pages ? __ldg(table + col) : -1;
     };
     auto locate = [&](int st, int tok, int pid) -> Where {
         Where w{0u, 0u, 1.f, 1.f};
-        const bool ok = (uint32_t)pid < (uint32_t)c.n_pages;
+        const bool is = (STEP == 32 || lane < STEP) && st * STEP + lane < n;
+        const bool ok = is && (uint32_t)pid < (uint32_t)c.n_pages;
         w.ok = __ballot_sync(0xffffffffu, ok);
         if (ok) {
             const uint32_t ph = (uint32_t)pid * c.hkv + h;
@@ -254,7 +274,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 w.ks = __ldg(c.K_scale + ph);
                 w.vs = __ldg(c.V_scale + ph);
             }
-        } else if ((STEP == 32 || lane < STEP) && st * STEP + lane < n) {
+        } else if (is) {
             latch(a.err, kErrDevice);
         }
         return w;
@@ -290,33 +310,25 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             }
         }
     };
-    int tok = fetch_token(step);
+    int pid = fetch_page(tok1);
     Where cur = locate(step, tok, fetch_page(tok));
 #pragma unroll
     for (int half = 0; half < TPS; ++half) {
         if (step < steps) gather(cur, half, ring);
         cp_async_commit();
     }
-    tok = fetch_token(step + stride);
-    int pid = fetch_page(tok);
-    int tok2 = fetch_token(step + 2 * stride);
+    int tok2 = fetch_token(step + 2 * stride, n);
 
     // ---- queries: B fragments, k slots in the order the K pieces come in
     uint32_t qf[PQ][KS][NT][2];
     float qs[NT][2];                                  // factor of the scores of heads 8 nt + 2 t, + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const T* q = static_cast<const T*>(a.Q) + q0 + (int64_t)(8 * nt + g) * D;
-        float4 v[KS];
+        const float4* v = qv[nt];
         float top = 0.f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            // the 4 components of k step s in this thread: one word of codes, two of bf16
-            const int w = E4 ? s : 2 * s;
-            const int d0 = (64 * (w / 4) + 16 * t + 4 * (w % 4)) / (int)sizeof(CT);
-            v[s] = 8 * nt + g < gn ? load4(q + d0) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < KS; ++s)
             top = fmaxf(top, fmaxf(fmaxf(fabsf(v[s].x), fabsf(v[s].y)), fmaxf(fabsf(v[s].z), fabsf(v[s].w))));
-        }
         float up = 1.f, down = 1.f;
         if (E4) {
             // largest component to [2^14, 2^15): fp16's subnormals begin 2^-28 below it
@@ -365,10 +377,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     int32_t flip = BUFFER;
     for (; step < steps; step += stride) {
         // the next step's rows into the buffer that the last one left
-        const Where next = locate(step + stride, tok, pid);
-        tok = tok2;
-        pid = fetch_page(tok);
-        tok2 = fetch_token(step + 3 * stride);
+        const Where next = locate(step + stride, tok1, pid);
+        tok1 = tok2;
+        pid = fetch_page(tok1);
+        tok2 = fetch_token(step + 3 * stride, n);
 #pragma unroll
         for (int half = 0; half < TPS; ++half) {
             if (step + stride < steps) gather(next, half, ahead);
@@ -545,98 +557,129 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     }
     cp_async_wait<0>();
 
-    // ---- merge the warps
+    // ---- every warp puts its sums where its rows were
+    __syncwarp();
+    float* mine = reinterpret_cast<float*>(ring_s + warp * 2 * BUFFER);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            const int head = 8 * nt + 2 * t + e;
             float s = l[nt][e];
             s += __shfl_xor_sync(0xffffffffu, s, 4);
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
             if (g == 0) {
-                m_s[warp][8 * nt + 2 * t + e] = unset[nt][e] ? -INFINITY : m[nt][e];
-                l_s[warp][8 * nt + 2 * t + e] = s;
+                m_s[warp][head] = unset[nt][e] ? -INFINITY : m[nt][e];
+                l_s[warp][head] = s;
             }
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                *reinterpret_cast<float2*>(mine + head * LD + pair_at(pair_of<D, (int)sizeof(CT)>(i, g))) =
+                    make_float2(o[i][nt][e], o[i][nt][e + 2]);
         }
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-        if (warp == w) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int head = 8 * nt + 2 * t + e;
-                    float M = m_s[0][head];
-#pragma unroll
-                    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, m_s[i][head]);
-                    const float f = unset[nt][e] ? 0.f : ex2(m[nt][e] - M);
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        // component(i, g) and the next, at the places [i][g]
-                        float2* p = reinterpret_cast<float2*>(acc_s + head * LD + 16 * i + 2 * g);
-                        float2 s = make_float2(f * o[i][nt][e], f * o[i][nt][e + 2]);
-                        if (w > 0) {
-                            const float2 old = *p;
-                            s.x += old.x;
-                            s.y += old.y;
-                        }
-                        *p = s;
-                    }
-                }
-        }
-        __syncthreads();
-    }
-    if (tid < HG) {
-        float M = m_s[0][tid], L = 0.f;
-#pragma unroll
-        for (int i = 1; i < kWarps; ++i) M = fmaxf(M, m_s[i][tid]);
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) L += (M == -INFINITY ? 0.f : ex2(m_s[i][tid] - M)) * l_s[i][tid];
-        mc_s[tid] = M;
-        lc_s[tid] = L;
-    }
-    // ---- merge the cluster: every CTA reads all of them and writes a share of the outputs
-    cg::cluster_group cluster = cg::this_cluster();
-    if (a.cluster > 1) cluster.sync();
+    if (alone) __syncwarp();
     else __syncthreads();
-    if (tid < HG) {
-        float M = -INFINITY, L = 0.f;
-        for (int i = 0; i < a.cluster; ++i) M = fmaxf(M, cluster.map_shared_rank(mc_s, i)[tid]);
-        for (int i = 0; i < a.cluster; ++i) {
-            const float f = M == -INFINITY ? 0.f : ex2(cluster.map_shared_rank(mc_s, i)[tid] - M);
-            f_s[i][tid] = f;
-            L += f * cluster.map_shared_rank(lc_s, i)[tid];
+    // ---- merge the warps: a head's pairs are taken by as many threads as there are for it
+    const int w0 = alone ? warp : 0, w1 = alone ? warp + 1 : kWarps;
+    const int per_head = (alone ? 32 : kThreads) / HG, id = alone ? lane : tid;
+    const int head = id / per_head;
+    float M = -INFINITY, L = 0.f, f[kWarps];
+    for (int w = w0; w < w1; ++w) M = fmaxf(M, m_s[w][head]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        f[w] = 0.f;
+        if (w >= w0 && w < w1 && M != -INFINITY) {
+            f[w] = ex2(m_s[w][head] - M);
+            L += f[w] * l_s[w][head];
         }
-        mt_s[tid] = M;
-        lt_s[tid] = L;
     }
-    __syncthreads();
-    for (int e = rank * kThreads + tid; e < gn * D; e += a.cluster * kThreads) {
-        const int head = e / D, d = e % D;
-        const int at = head * LD + place<ROWB, (int)sizeof(CT)>(d);
-        float s = 0.f;
-        for (int i = 0; i < a.cluster; ++i) s += f_s[i][head] * cluster.map_shared_rank(acc_s, i)[at];
-        const float L = lt_s[head];
-        put(static_cast<T*>(a.O) + q0 + e, L == 0.f ? 0.f : s / L);
+    const float* part = reinterpret_cast<const float*>(ring_s) + head * LD;
+    T* out = static_cast<T*>(a.O) + q0;
+    auto pair_sum = [&](int q) {
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            if (w >= w0 && w < w1) {
+                const float2 v = *reinterpret_cast<const float2*>(part + w * (2 * BUFFER / 4) + pair_at(q));
+                s.x += f[w] * v.x;
+                s.y += f[w] * v.y;
+            }
+        return s;
+    };
+    if (a.cluster == 1) {
+        if (head >= gn) return;
+        for (int q = id % per_head; q < D / 2; q += per_head) {
+            const float2 s = pair_sum(q);
+            put2(out + head * D + 2 * q, L == 0.f ? 0.f : s.x / L, L == 0.f ? 0.f : s.y / L);
+        }
+        if (a.lse && id % per_head == 0)
+            a.lse[q0 / D + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        return;
     }
-    if (a.lse && rank == 0 && tid < gn) {
-        const float L = lt_s[tid];
-        a.lse[q0 / D + tid] = L == 0.f ? -INFINITY : (mt_s[tid] + log2f(L)) * 0.69314718055994531f;
+    // ---- merge the cluster: CTA r writes share r of the outputs, the others send it theirs
+    cg::cluster_group cluster = cg::this_cluster();
+    const int share = HG * D / 2 / a.cluster;
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    for (int q = id % per_head; q < D / 2; q += per_head) {
+        const int e = head * (D / 2) + q;
+        cluster.map_shared_rank(sum_r, e / share)[rank * share + e % share] = pair_sum(q);
     }
-    if (a.cluster > 1) cluster.sync();
+    if (id % per_head == 0)
+        for (int r = 0; r < a.cluster; ++r) {
+            cluster.map_shared_rank(&m_r[0][0], r)[rank * HG + head] = M;
+            cluster.map_shared_rank(&l_r[0][0], r)[rank * HG + head] = L;
+        }
+    cluster.sync();
+    for (int j = tid; j < share; j += kThreads) {
+        const int e = rank * share + j, hd = e / (D / 2), q = e % (D / 2);
+        if (hd >= gn) break;
+        float top = -INFINITY, sum = 0.f;
+        for (int r = 0; r < a.cluster; ++r) top = fmaxf(top, m_r[r][hd]);
+        float2 s = make_float2(0.f, 0.f);
+        for (int r = 0; r < a.cluster; ++r) {
+            const float fr = top == -INFINITY ? 0.f : ex2(m_r[r][hd] - top);
+            const float2 v = sum_r[r * share + j];
+            sum += fr * l_r[r][hd];
+            s.x += fr * v.x;
+            s.y += fr * v.y;
+        }
+        put2(out + hd * D + 2 * q, sum == 0.f ? 0.f : s.x / sum, sum == 0.f ? 0.f : s.y / sum);
+        if (a.lse && q == 0) a.lse[q0 / D + hd] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    }
+}
+
+int sm_count() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
 }
 
 template <int D, typename CT, typename T, int NT>
 int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     a.groups = (a.G + 8 * NT - 1) / (8 * NT);
     const int64_t units = rows * a.groups;
-    // few rows: a cluster of CTAs shares each, as long as every warp has a step
-    const int steps = (a.max_sel + 31) / 32;
+    a.units = (uint32_t)units;
+    const int step = 16 * tiles_per_step<D, CT>();
+    const int64_t steps = (a.max_sel + step - 1) / step;
+    const int64_t resident = (int64_t)min_ctas<D, CT, T, NT>() * sm_count();
+    // Few rows: a cluster of CTAs shares each, while all of them fit on the GPU at
+    // once and every warp has a step (4 rows of 4,160 tokens, 16 heads of 128:
+    // 10.5 us with 8 CTAs a row, 33 with one; 128 rows of 1,600: 10.2 with 2, 12.4
+    // with one, 13.6 with 4).
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && units * a.cluster < 2 * 148 && a.cluster * 2 * kWarps <= steps) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && units * a.cluster * 2 <= resident && a.cluster * 2 * kWarps <= steps) a.cluster *= 2;
+    // Many rows: a warp takes a whole one, which needs no merge, unless the last
+    // round of warps would then run long.  In microseconds a CTA that shares a row
+    // takes about 4 + steps / 4, four whole rows side by side 6 + steps (8 heads of
+    // 128, 8-bit pages; 4,096 rows of 64 tokens: 41 us shared, 22 whole; 16,384 of
+    // 512: 320 and 247; 1,024 of 2,048: 64 and 73).
+    const int64_t shared = (units + resident - 1) / resident * (4 + (steps + kWarps - 1) / kWarps);
+    const int64_t whole = (units + kWarps * resident - 1) / (kWarps * resident) * (6 + steps);
+    a.warps = a.cluster == 1 && whole < shared ? 1 : kWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * a.cluster));
+    cfg.gridDim = dim3((unsigned)(a.warps == 1 ? (units + kWarps - 1) / kWarps : units * a.cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.dynamicSmemBytes = (size_t)kWarps * 2 * tiles_per_step<D, CT>() * 32 * D * sizeof(CT);
