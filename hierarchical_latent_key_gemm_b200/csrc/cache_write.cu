@@ -14,16 +14,18 @@
 // turn in fp64, and its sine and cosine are taken in fp32 with the rest of the
 // reduction added to first order.
 //
-// Work: one CTA per (page that a sequence writes, range of heads).  A row
+// Work: one CTA per (page that a sequence writes, range of its lists).  A row
 // (token, head) is taken by d/16 threads, each holding two 8-element pieces
-// whose elements are each other's partners, so a pair never leaves a thread;
-// the sines of a token are kept in registers for all its heads.
+// whose elements are each other's partners, so a pair never leaves a thread.
+#include <algorithm>
+
 #include "cache_common.cuh"
 
 namespace lsa {
 namespace {
 
 constexpr int kWriteThreads = 256;
+constexpr int kMaxPageThreads = 512;
 
 struct WriteArgs {
     CacheArgs c;
@@ -38,41 +40,66 @@ struct WriteArgs {
     int64_t n;
     int batch, hq, rot, interleaved;
     int by_token;          // units are tokens (few of them) instead of page slots
-    int tokens_per_pass;   // tokens of a page that a CTA takes at a time (a power of two)
-    int kv_per, q_per;     // heads of a CTA (blockIdx.y)
+    int most_tokens;       // of a unit
+    int lists;             // rows of a token: its K heads, its V heads, its query heads
+    // blockIdx.y, few tokens a page: per_cta lists each; whole pages: kv_ctas CTAs
+    // with kv_per KV heads each, then others with q_per query heads each, q_side of
+    // them side by side
+    int per_cta, kv_ctas, kv_per, q_per, q_side;
     int32_t* err;
 };
 
-// ---- 8 elements at a time
-__device__ __forceinline__ void load8(const float* p, float* x) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// ---- a piece: 8 elements of a row, two runs of 4 that are `gap` elements apart.
+// Loaded as they are, unpacked where they are used.  bf16 pieces are 16 bytes in
+// one run (gap 4); of fp32 rows the 16 bytes of a run are neighbours of the next
+// thread's.
+template <typename T>
+struct Piece {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p, int gap) {
+        w[0] = *reinterpret_cast<const uint4*>(p);
+        if constexpr (sizeof(T) == 4) w[1] = *reinterpret_cast<const uint4*>(p + gap);
     }
+    __device__ __forceinline__ void unpack(float* x) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[4 * i] = __uint_as_float(w[i].x);
+                x[4 * i + 1] = __uint_as_float(w[i].y);
+                x[4 * i + 2] = __uint_as_float(w[i].z);
+                x[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        } else {
+            const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(v[i] << 16);
+                x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
+// 8 elements to a row of the activations' type or of bf16 pages
+__device__ __forceinline__ void store8(float* p, const float* x, int gap) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    *reinterpret_cast<float4*>(p + gap) = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x, int gap) {
+    const uint2 u = make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+    const uint2 v = make_uint2(bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+    if (gap == 4) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(u.x, u.y, v.x, v.y);
+    } else {
+        *reinterpret_cast<uint2*>(p) = u;
+        *reinterpret_cast<uint2*>(p + gap) = v;
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 // 8-bit pages: x times the inverse scale, values that are not finite as NaN
-__device__ __forceinline__ void store8(uint8_t* p, const float* x, float inv) {
+__device__ __forceinline__ void store8(uint8_t* p, const float* x, int gap, float inv) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -84,7 +111,12 @@ __device__ __forceinline__ void store8(uint8_t* p, const float* x, float inv) {
         }
         w[i] = (uint32_t)f32x2_to_e4m3x2(y[0], y[1]) | ((uint32_t)f32x2_to_e4m3x2(y[2], y[3]) << 16);
     }
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    if (gap == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+        *reinterpret_cast<uint32_t*>(p + gap) = w[1];
+    }
 }
 
 // largest finite magnitude of 8 elements, at least m
@@ -107,24 +139,24 @@ __device__ __forceinline__ int scale_exp(float amax, float lim_m) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// cos and sin of 8 pairs at position t
-__device__ __forceinline__ void turn8(const double* inv_freq, int64_t t, float* cs, float* sn) {
+// cos and sin of 8 pairs at position t: pairs p, p + 1, .. up to the next multiple
+// of `run`, then those `hop` pairs on, and so forth
+__device__ __forceinline__ void turn8(const double* inv_freq, int p, int run, int hop, int64_t t, float* cs, float* sn) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const double th = (double)t * inv_freq[i];
-        // r = th - 2 pi k, |r| <= pi, with 2 pi in two parts
-        const double k = rint(th * 0.15915494309189535);
-        const double r = fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586, th));
+        // half turns, less whole turns: r in [-1, 1], exact but for the two products
+        const double th = (double)t * inv_freq[p + i % run + i / run * hop] * 0.31830988618379067;
+        const double r = fma(-2.0, rint(0.5 * th), th);
         const float hi = (float)r;
-        const float lo = (float)(r - (double)hi);
+        const float lo = (float)(r - (double)hi) * 3.14159274f;
         float s, c;
-        sincosf(hi, &s, &c);
+        sincospif(hi, &s, &c);
         cs[i] = fmaf(-lo, s, c);
         sn[i] = fmaf(lo, c, s);
     }
 }
 
-// Turn the pairs of pieces a and b (see piece_a, piece_b).
+// Turn the pairs of pieces a and b.
 __device__ __forceinline__ void rotate16(float* a, float* b, const float* cs, const float* sn, bool interleaved) {
     if (interleaved) {
 #pragma unroll
@@ -145,21 +177,23 @@ __device__ __forceinline__ void rotate16(float* a, float* b, const float* cs, co
     }
 }
 
-template <int D, typename T, typename CT>
-__global__ __launch_bounds__(kWriteThreads) void cache_write_kernel(const WriteArgs a) {
-    constexpr bool kScaled = sizeof(CT) == 1;
-    constexpr int TPR = D / 16;                     // threads per row
-    constexpr int ROWS = kWriteThreads / TPR;
-    extern __shared__ uint32_t sm[];                // [2][kv_per] largest magnitudes, then scales
-    __shared__ int found_b, broken;
-    const int tid = threadIdx.x;
-    const CacheArgs& c = a.c;
+// What a CTA writes: rows [r0, r0 + m) of one sequence, the first of them token
+// `pos`, all in one page from slot `slot0` on.
+struct Unit {
+    int64_t r0, pos;
+    int m, slot0, pid;
+};
 
-    // the sequence of this unit, all sequences checked on the way
+// The unit of this CTA (blockIdx.x); false where there is none.  Every CTA looks
+// all sequences over, so that a broken cu stops all of them.
+__device__ __forceinline__ bool find_unit(const WriteArgs& a, Unit& u) {
+    __shared__ int found_b, broken;
+    const CacheArgs& c = a.c;
+    const int tid = threadIdx.x;
     if (tid == 0) { found_b = -1; broken = 0; }
     __syncthreads();
     const int64_t x = blockIdx.x;
-    for (int b = tid; b < a.batch; b += kWriteThreads) {
+    for (int b = tid; b < a.batch; b += blockDim.x) {
         const int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
         if (c0 < 0 || c1 < c0 || c1 > a.n) broken = 1;
         const int64_t u0 = a.by_token ? c0 : (c0 >> c.log2_page) + 2 * (int64_t)b;
@@ -167,153 +201,411 @@ __global__ __launch_bounds__(kWriteThreads) void cache_write_kernel(const WriteA
         if (x >= u0 && x < u1) found_b = b;
     }
     __syncthreads();
+    const int b = found_b;
     if (broken) {
         if (tid == 0) latch(a.err, kErrDevice);
-        return;
+        return false;
     }
-    const int b = found_b;
-    if (b < 0) return;
+    if (b < 0) return false;
     const int64_t c0 = a.cu[b], c1 = a.cu[b + 1], p0 = a.pos0[b];
     if (p0 < 0) {
         if (tid == 0) latch(a.err, kErrDevice);
-        return;
+        return false;
     }
-    // the unit's rows [r0, r0 + m) and their first slot
-    int64_t r0;
     if (a.by_token) {
-        r0 = x;
-        if (r0 > c0 && ((p0 + r0 - c0) & (c.page - 1)) != 0) return;   // not the first new token of its page
+        u.r0 = x;
+        if (u.r0 > c0 && ((p0 + u.r0 - c0) & (c.page - 1)) != 0) return false;   // not its page's first new token
     } else {
         const int64_t pg = (p0 >> c.log2_page) + (x - ((c0 >> c.log2_page) + 2 * (int64_t)b));
-        r0 = max(c0, c0 + (pg << c.log2_page) - p0);
+        u.r0 = max(c0, c0 + (pg << c.log2_page) - p0);
     }
-    if (r0 >= c1) return;
-    const int64_t pos = p0 + r0 - c0;
-    const int slot0 = (int)(pos & (c.page - 1));
-    const int m = (int)min((int64_t)(c.page - slot0), c1 - r0);
-    const int pid = cache_page(c, b, pos);
-    if (pid < 0) {
+    if (u.r0 >= c1) return false;
+    u.pos = p0 + u.r0 - c0;
+    u.slot0 = (int)(u.pos & (c.page - 1));
+    u.m = (int)min((int64_t)(c.page - u.slot0), c1 - u.r0);
+    u.pid = cache_page(c, b, u.pos);
+    if (u.pid < 0) {
         if (tid == 0) latch(a.err, kErrDevice);
-        return;
+        return false;
     }
+    return true;
+}
 
-    const int piece = tid % TPR, row = tid / TPR;
-    const int TT = a.tokens_per_pass, HT = ROWS / TT;
-    const int hh = row % HT, tt = row / HT;
-    const int kv0 = blockIdx.y * a.kv_per, kv1 = min(c.hkv, kv0 + a.kv_per);
-    const int q0 = blockIdx.y * a.q_per, q1 = min(a.hq, q0 + a.q_per);
-    // this thread's two 8-element pieces of a K or Q row: partners of each other
-    const bool turned = piece < a.rot / 16;
-    const int pa = turned && !a.interleaved ? 8 * piece : 16 * piece;
-    const int pb = turned && !a.interleaved ? 8 * piece + a.rot / 2 : 16 * piece + 8;
+// A list: one head's rows of K, V or Q.  A token's lists are its K heads [0, hkv),
+// its V heads [hkv, 2 hkv), its query heads from 2 hkv on.
+template <typename T>
+struct List {
+    const T* src;          // row r0
+    T* out;                // where the (rotated) row r0 goes, or null
+    int64_t step;          // elements from one token to the next
+    int h;                 // head
+    bool is_k, is_v;
+};
+template <int D, typename T>
+__device__ __forceinline__ List<T> list_of(const WriteArgs& a, int64_t r0, int l) {
+    const int hkv = a.c.hkv;
+    List<T> s;
+    s.is_k = l < hkv;
+    s.is_v = !s.is_k && l < 2 * hkv;
+    const bool q = l >= 2 * hkv;
+    const int heads = q ? a.hq : hkv;
+    s.h = q ? l - 2 * hkv : s.is_v ? l - hkv : l;
+    s.step = (int64_t)heads * D;
+    const int64_t off = (r0 * heads + s.h) * D;
+    s.src = static_cast<const T*>(q ? a.Q : s.is_v ? a.V : a.K) + off;
+    T* out = static_cast<T*>(q ? a.Q_out : s.is_v ? nullptr : a.K_out);
+    s.out = out ? out + off : nullptr;
+    return s;
+}
 
-    const T* K = static_cast<const T*>(a.K);
-    const T* V = static_cast<const T*>(a.V);
-    float* scales = reinterpret_cast<float*>(sm);
-    if (kScaled) {
-        for (int i = tid; i < 2 * a.kv_per; i += kWriteThreads) sm[i] = 0;
-        __syncthreads();
-        for (int h = kv0 + hh; h < kv1; h += HT) {
-            float mk = 0.f, mv = 0.f;
-            for (int t = tt; t < m; t += TT) {
-                const int64_t o = ((r0 + t) * c.hkv + h) * D + 16 * piece;
-                float v[8];
-                load8(K + o, v);
-                mk = amax8(v, mk);
-                load8(K + o + 8, v);
-                mk = amax8(v, mk);
-                load8(V + o, v);
-                mv = amax8(v, mv);
-                load8(V + o + 8, v);
-                mv = amax8(v, mv);
-            }
-            // magnitudes are >= 0: their bit patterns order like the values
-            atomicMax(&sm[h - kv0], __float_as_uint(mk));
-            atomicMax(&sm[a.kv_per + h - kv0], __float_as_uint(mv));
-        }
-        __syncthreads();
-        for (int i = tid; i < 2 * (kv1 - kv0); i += kWriteThreads) {
-            const bool is_v = i >= kv1 - kv0;
-            const int h = is_v ? i - (kv1 - kv0) : i;
-            const int j = (is_v ? a.kv_per : 0) + h;
-            float* gs = (is_v ? c.V_scale : c.K_scale) + (int64_t)pid * c.hkv + kv0 + h;
-            float s = pow2i(scale_exp(__uint_as_float(sm[j]), is_v ? 1.75f : 1.234375f));   // 448, 316 = that * 2^8
-            if (slot0 > 0) {
-                const float old = *gs;
-                if (s > old) {
-                    // what the page holds, under the larger scale
-                    uint8_t* p = static_cast<uint8_t*>(is_v ? c.V : c.K) + cache_row(c, pid, kv0 + h, 0) * D;
-                    const float ratio = old / s;
-                    for (int e = 0; e < slot0 * D; e += 8) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(p + e);
-                        const float4 f0 = e4m3x4_to_f32x4(w.x), f1 = e4m3x4_to_f32x4(w.y);
-                        const float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                        store8(p + e, v, ratio);
-                    }
-                } else {
-                    s = old;
-                }
-            }
-            *gs = s;
-            scales[j] = 1.f / s;
-        }
-        __syncthreads();
+// Where the scale of K or V list s of the unit's page is.
+template <typename T>
+__device__ __forceinline__ float* scale_at(const WriteArgs& a, const Unit& u, const List<T>& s) {
+    return (s.is_v ? a.c.V_scale : a.c.K_scale) + (int64_t)u.pid * a.c.hkv + s.h;
+}
+// The scale that the largest finite magnitude written asks for; 448 = 1.75 * 2^8, 316 = 1.234375 * 2^8.
+__device__ __forceinline__ float new_scale(float top, bool is_v) {
+    return pow2i(scale_exp(top, is_v ? 1.75f : 1.234375f));
+}
+
+// What the page holds below slot0, under the larger scale.  All threads of the CTA.
+template <int D, typename T>
+__device__ __forceinline__ void shrink_held(const WriteArgs& a, const Unit& u, const List<T>& s, float shrink) {
+    uint8_t* p = static_cast<uint8_t*>(s.is_v ? a.c.V : a.c.K) + cache_row(a.c, u.pid, s.h, 0) * D;
+    for (int e = 8 * threadIdx.x; e < u.slot0 * D; e += 8 * blockDim.x) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p + e);
+        const float4 f0 = e4m3x4_to_f32x4(w.x), f1 = e4m3x4_to_f32x4(w.y);
+        const float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+        store8(p + e, v, 4, shrink);
     }
+}
 
-    for (int t = tt; t < m; t += TT) {
-        float cs[8], sn[8];
-        if (turned) turn8(a.inv_freq + 8 * piece, pos + t, cs, sn);
-        for (int h = kv0 + hh; h < kv1; h += HT) {
-            const int64_t o = ((r0 + t) * c.hkv + h) * D;
-            CT* kp = static_cast<CT*>(c.K) + cache_row(c, pid, h, slot0 + t) * D;
-            CT* vp = static_cast<CT*>(c.V) + cache_row(c, pid, h, slot0 + t) * D;
-            float u[8], v[8];
-            load8(K + o + pa, u);
-            load8(K + o + pb, v);
-            if (turned) rotate16(u, v, cs, sn, a.interleaved);
-            if (a.K_out) {
-                store8(static_cast<T*>(a.K_out) + o + pa, u);
-                store8(static_cast<T*>(a.K_out) + o + pb, v);
-            }
-            if constexpr (kScaled) {
-                store8(kp + pa, u, scales[h - kv0]);
-                store8(kp + pb, v, scales[h - kv0]);
-            } else {
-                store8(kp + pa, u);
-                store8(kp + pb, v);
-            }
-            load8(V + o + 16 * piece, u);
-            load8(V + o + 16 * piece + 8, v);
-            if constexpr (kScaled) {
-                store8(vp + 16 * piece, u, scales[a.kv_per + h - kv0]);
-                store8(vp + 16 * piece + 8, v, scales[a.kv_per + h - kv0]);
-            } else {
-                store8(vp + 16 * piece, u);
-                store8(vp + 16 * piece + 8, v);
-            }
-        }
-        for (int h = q0 + hh; h < q1; h += HT) {
-            const int64_t o = ((r0 + t) * a.hq + h) * D;
-            float u[8], v[8];
-            load8(static_cast<const T*>(a.Q) + o + pa, u);
-            load8(static_cast<const T*>(a.Q) + o + pb, v);
-            if (turned) rotate16(u, v, cs, sn, a.interleaved);
-            store8(static_cast<T*>(a.Q_out) + o + pa, u);
-            store8(static_cast<T*>(a.Q_out) + o + pb, v);
+// Where this thread's two pieces of a row are: the same pairs' components in K
+// and Q, anything in V.
+struct Pieces {
+    int a, b, gap;         // of K and Q rows
+    int va, vb, vgap;      // of V rows
+    int piece;
+    bool turned;
+    __device__ __forceinline__ int first(bool is_v) const { return is_v ? va : a; }
+    __device__ __forceinline__ int second(bool is_v) const { return is_v ? vb : b; }
+    __device__ __forceinline__ int step(bool is_v) const { return is_v ? vgap : gap; }
+};
+template <int D, typename T>
+__device__ __forceinline__ Pieces pieces_of(const WriteArgs& a, int piece) {
+    constexpr int TPR = D / 16;
+    const int n8 = a.rot / 16;                     // threads of a row that turn something
+    Pieces p;
+    p.piece = piece;
+    p.turned = piece < n8;
+    if constexpr (sizeof(T) == 4) {
+        const int n = p.turned ? n8 : TPR - n8;    // threads that share the turned or the other components
+        p.gap = 4 * n;
+        p.a = p.turned ? 4 * piece : a.rot + 4 * (piece - n8);
+        p.b = p.a + 8 * n;                         // turned halves: rot / 2 = 8 n8 apart, too
+        p.va = 4 * piece;
+        p.vb = p.va + 8 * TPR;
+        p.vgap = 4 * TPR;
+    } else {
+        p.gap = p.vgap = 4;
+        p.a = p.turned && !a.interleaved ? 8 * piece : 16 * piece;
+        p.b = p.turned && !a.interleaved ? p.a + a.rot / 2 : p.a + 8;
+        p.va = 16 * piece;
+        p.vb = p.va + 8;
+    }
+    return p;
+}
+
+// Store one row's pieces (token r0 + t of the unit), turned already.
+template <int D, typename T, typename CT>
+__device__ __forceinline__ void store_row(const WriteArgs& a, const Unit& u, const List<T>& s, const Pieces& pc, int t,
+                                          const float* x, const float* y, float inv) {
+    const int oa = pc.first(s.is_v), ob = pc.second(s.is_v), gap = sizeof(T) == 4 ? pc.step(s.is_v) : 4;
+    if (s.out) {
+        store8(s.out + t * s.step + oa, x, gap);
+        store8(s.out + t * s.step + ob, y, gap);
+    }
+    if (s.is_k || s.is_v) {
+        CT* p = static_cast<CT*>(s.is_v ? a.c.V : a.c.K) + cache_row(a.c, u.pid, s.h, u.slot0 + t) * D;
+        if constexpr (sizeof(CT) == 1) {
+            store8(p + oa, x, gap, inv);
+            store8(p + ob, y, gap, inv);
+        } else {
+            store8(p + oa, x, gap);
+            store8(p + ob, y, gap);
         }
     }
 }
 
+// Sines and cosines of the unit's tokens, for all their heads: [token][4][rot / 16]
+// float4, cos 0-3, cos 4-7, sin 0-3, sin 4-7 of 8 pairs.
+template <typename T>
+__device__ __forceinline__ void fill_turns(const WriteArgs& a, const Unit& u, float4* turns) {
+    const int n8 = a.rot / 16;
+    for (int i = threadIdx.x; i < u.m * n8; i += blockDim.x) {
+        const int t = i / n8, p = i % n8;
+        float cs[8], sn[8];
+        // the pairs of pieces a and b (see pieces_of)
+        if (sizeof(T) == 2) turn8(a.inv_freq, 8 * p, 8, 0, u.pos + t, cs, sn);
+        else if (a.interleaved) turn8(a.inv_freq, 2 * p, 2, 2 * n8, u.pos + t, cs, sn);
+        else turn8(a.inv_freq, 4 * p, 4, 4 * n8, u.pos + t, cs, sn);
+        float4* at = turns + t * 4 * n8 + p;
+        at[0] = make_float4(cs[0], cs[1], cs[2], cs[3]);
+        at[n8] = make_float4(cs[4], cs[5], cs[6], cs[7]);
+        at[2 * n8] = make_float4(sn[0], sn[1], sn[2], sn[3]);
+        at[3 * n8] = make_float4(sn[4], sn[5], sn[6], sn[7]);
+    }
+}
+// Turn the pieces x, y of a row of token t.
+__device__ __forceinline__ void turn_row(const WriteArgs& a, const float4* turns, const Pieces& pc, int t, float* x,
+                                         float* y) {
+    const int n8 = a.rot / 16;
+    const float4* at = turns + t * 4 * n8 + pc.piece;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float4 c4 = at[k * n8], s4 = at[(2 + k) * n8];
+        cs[4 * k] = c4.x; cs[4 * k + 1] = c4.y; cs[4 * k + 2] = c4.z; cs[4 * k + 3] = c4.w;
+        sn[4 * k] = s4.x; sn[4 * k + 1] = s4.y; sn[4 * k + 2] = s4.z; sn[4 * k + 3] = s4.w;
+    }
+    rotate16(x, y, cs, sn, a.interleaved);
+}
+
+// Few tokens a page: the unit's rows (token, list) in order, ROWS side by side.
+// The largest magnitudes of 8-bit pages take a pass of their own.
 template <int D, typename T, typename CT>
-int launch(const WriteArgs& a, dim3 grid, cudaStream_t s) {
+__global__ __launch_bounds__(kWriteThreads) void cache_write_few_kernel(const WriteArgs a) {
+    constexpr bool kScaled = sizeof(CT) == 1;
+    constexpr int TPR = D / 16;                     // threads per row
+    constexpr int ROWS = kWriteThreads / TPR;
+    extern __shared__ float4 turn_s[];              // then [per_cta] largest magnitudes or inverse scales, [per_cta] shrinks
+    uint32_t* top_s = reinterpret_cast<uint32_t*>(turn_s + a.most_tokens * (a.rot / 4));
+    float *inv_s = reinterpret_cast<float*>(top_s), *shrink_s = inv_s + a.per_cta;
+    Unit u;
+    if (!find_unit(a, u)) return;
+    const int tid = threadIdx.x, row = tid / TPR;
+    const Pieces pc = pieces_of<D, T>(a, tid % TPR);
+    const int l0 = blockIdx.y * a.per_cta, l1 = min(a.lists, l0 + a.per_cta);
+    const int le = kScaled ? max(l0, min(l1, 2 * a.c.hkv)) : l0;    // lists with a scale
+    fill_turns<T>(a, u, turn_s);
+    for (int i = tid; i < le - l0; i += kWriteThreads) top_s[i] = 0;
+    __syncthreads();
+    if (l0 < le) {
+        const int lists = le - l0;
+        for (int r = row; r < u.m * lists; r += ROWS) {
+            const int t = r / lists, l = l0 + r % lists;
+            const List<T> s = list_of<D, T>(a, u.r0, l);
+            Piece<T> x, y;
+            x.load(s.src + t * s.step + pc.va, pc.vgap);
+            y.load(s.src + t * s.step + pc.vb, pc.vgap);
+            float v[8];
+            x.unpack(v);
+            float top = amax8(v, 0.f);
+            y.unpack(v);
+            top = amax8(v, top);
+            // only the threads of one row run the same trips of this loop
+            const uint32_t row_mask = ((1u << TPR) - 1u) << ((tid & 31) / TPR * TPR);
+#pragma unroll
+            for (int i = 1; i < TPR; i *= 2) top = fmaxf(top, __shfl_xor_sync(row_mask, top, i));
+            // magnitudes are >= 0: their bit patterns order like the values
+            if (pc.piece == 0) atomicMax(&top_s[l - l0], __float_as_uint(top));
+        }
+        __syncthreads();
+        for (int l = l0 + tid; l < le; l += kWriteThreads) {
+            const List<T> s = list_of<D, T>(a, u.r0, l);
+            const float old = u.slot0 > 0 ? *scale_at(a, u, s) : 0.f;
+            const float scale = fmaxf(new_scale(__uint_as_float(top_s[l - l0]), s.is_v), old);
+            *scale_at(a, u, s) = scale;
+            inv_s[l - l0] = 1.f / scale;
+            shrink_s[l - l0] = old / scale;
+        }
+        __syncthreads();
+        if (u.slot0 > 0)
+            for (int l = l0; l < le; ++l)
+                if (shrink_s[l - l0] != 1.f) shrink_held<D, T>(a, u, list_of<D, T>(a, u.r0, l), shrink_s[l - l0]);
+    }
+    const int lists = l1 - l0;
+    for (int r = row; r < u.m * lists; r += ROWS) {
+        const int t = r / lists, l = l0 + r % lists;
+        const List<T> s = list_of<D, T>(a, u.r0, l);
+        Piece<T> x, y;
+        x.load(s.src + t * s.step + pc.first(s.is_v), pc.step(s.is_v));
+        y.load(s.src + t * s.step + pc.second(s.is_v), pc.step(s.is_v));
+        float v[8], w[8];
+        x.unpack(v);
+        y.unpack(w);
+        if (pc.turned && !s.is_v) turn_row(a, turn_s, pc, t, v, w);
+        store_row<D, T, CT>(a, u, s, pc, t, v, w, l < le ? inv_s[l - l0] : 1.f);
+    }
+}
+
+// Whole pages.  blockIdx.y: CTAs for KV heads, then CTAs for query heads.  A KV
+// head's K and V rows of the page are in registers while their scales are
+// settled, two tokens a thread, so they are read once; queries stream through,
+// several rows on their way in every thread.
+template <typename T>
+constexpr int rows_ahead() { return sizeof(T) == 4 ? 4 : 8; }
+template <int D, typename T, typename CT>
+__global__ __launch_bounds__(kMaxPageThreads) void cache_write_page_kernel(const WriteArgs a) {
+    constexpr bool kScaled = sizeof(CT) == 1;
+    constexpr int TPR = D / 16, kAhead = rows_ahead<T>();
+    const int ROWS = blockDim.x / TPR;              // a page has at most 2 ROWS tokens
+    extern __shared__ float4 turn_s[];              // then [kv_per][2] largest magnitudes
+    uint32_t* top_s = reinterpret_cast<uint32_t*>(turn_s + a.most_tokens * (a.rot / 4));
+    Unit u;
+    if (!find_unit(a, u)) return;
+    const int tid = threadIdx.x, row = tid / TPR;
+    const Pieces pc = pieces_of<D, T>(a, tid % TPR);
+    const int y = blockIdx.y;
+    fill_turns<T>(a, u, turn_s);
+    if (y < a.kv_ctas) {
+        const int h0 = y * a.kv_per, h1 = min(a.c.hkv, h0 + a.kv_per);
+        for (int i = tid; i < 2 * (h1 - h0); i += blockDim.x) top_s[i] = 0;
+        __syncthreads();
+        for (int h = h0; h < h1; ++h) {
+            const List<T> ks = list_of<D, T>(a, u.r0, h), vs = list_of<D, T>(a, u.r0, a.c.hkv + h);
+            Piece<T> k[2][2], v[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = row + i * ROWS;
+                if (t < u.m) {
+                    k[i][0].load(ks.src + t * ks.step + pc.a, pc.gap);
+                    k[i][1].load(ks.src + t * ks.step + pc.b, pc.gap);
+                    v[i][0].load(vs.src + t * vs.step + pc.va, pc.vgap);
+                    v[i][1].load(vs.src + t * vs.step + pc.vb, pc.vgap);
+                }
+            }
+            float ki = 1.f, vi = 1.f;
+            if constexpr (kScaled) {
+                const float k_old = u.slot0 > 0 ? *scale_at(a, u, ks) : 0.f;
+                const float v_old = u.slot0 > 0 ? *scale_at(a, u, vs) : 0.f;
+                float kt = 0.f, vt = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (row + i * ROWS < u.m) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float x[8];
+                            k[i][j].unpack(x);
+                            kt = amax8(x, kt);
+                            v[i][j].unpack(x);
+                            vt = amax8(x, vt);
+                        }
+                    }
+                // magnitudes are >= 0: their bit patterns order like the values
+                const uint32_t kb = __reduce_max_sync(0xffffffffu, __float_as_uint(kt));
+                const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vt));
+                uint32_t* top = top_s + 2 * (h - h0);
+                if (tid % 32 == 0) {
+                    atomicMax(&top[0], kb);
+                    atomicMax(&top[1], vb);
+                }
+                __syncthreads();                    // the old scales are read, too
+                const float k_new = fmaxf(new_scale(__uint_as_float(top[0]), false), k_old);
+                const float v_new = fmaxf(new_scale(__uint_as_float(top[1]), true), v_old);
+                if (tid == 0) {
+                    *scale_at(a, u, ks) = k_new;
+                    *scale_at(a, u, vs) = v_new;
+                }
+                if (u.slot0 > 0 && k_new > k_old) shrink_held<D, T>(a, u, ks, k_old / k_new);
+                if (u.slot0 > 0 && v_new > v_old) shrink_held<D, T>(a, u, vs, v_old / v_new);
+                ki = 1.f / k_new;
+                vi = 1.f / v_new;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = row + i * ROWS;
+                if (t < u.m) {
+                    float x[8], w[8];
+                    k[i][0].unpack(x);
+                    k[i][1].unpack(w);
+                    if (pc.turned) turn_row(a, turn_s, pc, t, x, w);
+                    store_row<D, T, CT>(a, u, ks, pc, t, x, w, ki);
+                    v[i][0].unpack(x);
+                    v[i][1].unpack(w);
+                    store_row<D, T, CT>(a, u, vs, pc, t, x, w, vi);
+                }
+            }
+        }
+        return;
+    }
+    __syncthreads();
+    // query heads: LT of a token's side by side, so that a warp's loads and stores are runs
+    const int h0 = (y - a.kv_ctas) * a.q_per, h1 = min(a.hq, h0 + a.q_per);
+    const int LT = a.q_side, TT = ROWS / LT;
+    const int hh = h0 + row % LT;
+    for (int t = row / LT; t < u.m; t += TT) {
+        const int64_t at = ((u.r0 + t) * a.hq + hh) * D;
+        const T* src = static_cast<const T*>(a.Q) + at;
+        T* out = static_cast<T*>(a.Q_out) + at;
+        // Q_out may be Q: a row's pieces are loaded before they are stored, and no two rows share elements
+        for (int h = hh; h < h1; h += kAhead * LT) {
+            Piece<T> x[kAhead], w[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (h + i * LT < h1) {
+                    x[i].load(src + i * LT * D + pc.a, pc.gap);
+                    w[i].load(src + i * LT * D + pc.b, pc.gap);
+                }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (h + i * LT < h1) {
+                    float p[8], q[8];
+                    x[i].unpack(p);
+                    w[i].unpack(q);
+                    if (pc.turned) turn_row(a, turn_s, pc, t, p, q);
+                    store8(out + i * LT * D + pc.a, p, pc.gap);
+                    store8(out + i * LT * D + pc.b, q, pc.gap);
+                }
+            src += kAhead * LT * D;
+            out += kAhead * LT * D;
+        }
+    }
+}
+
+template <typename K>
+int launch_with(K kernel, const WriteArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e);
     note_launch();
-    cache_write_kernel<D, T, CT><<<grid, kWriteThreads, 2 * (size_t)a.kv_per * sizeof(float), s>>>(a);
+    kernel<<<grid, threads, smem, s>>>(a);
     return cuda_status(cudaGetLastError());
 }
 
+template <int D, typename T, typename CT>
+int launch(WriteArgs a, int64_t units, bool pages, cudaStream_t s) {
+    const size_t turns = (size_t)a.most_tokens * (a.rot / 4) * sizeof(float4);
+    if (!pages) {
+        const int64_t want = 148 * 3;
+        // few units: their lists are split over CTAs, down to the rows that a CTA takes side by side
+        constexpr int ROWS = kWriteThreads / (D / 16);
+        const int64_t per_unit = std::max<int64_t>(1, std::min<int64_t>(a.c.page, a.n / a.batch));   // tokens, on average
+        const int64_t most = std::min<int64_t>((a.lists * per_unit + ROWS - 1) / ROWS, (want + units - 1) / units);
+        a.per_cta = (int)((a.lists + most - 1) / most);
+        const dim3 grid((unsigned)units, (unsigned)((a.lists + a.per_cta - 1) / a.per_cta));
+        return launch_with(cache_write_few_kernel<D, T, CT>, a, grid, kWriteThreads,
+                           turns + 2 * (size_t)a.per_cta * sizeof(float), s);
+    }
+    const int threads = std::min(kMaxPageThreads, std::max(64, a.c.page * (D / 16) / 2));
+    // few units: their heads are split over CTAs; a KV head is about three query heads' work
+    const int64_t want = 148 / 2 * kMaxPageThreads / threads;
+    const int64_t most = std::max<int64_t>(1, (want + units / 2) / units), work = 3 * a.c.hkv + a.hq;
+    const int64_t kv_ctas = std::min<int64_t>(a.c.hkv, std::max<int64_t>(1, (3 * a.c.hkv * most + work / 2) / work));
+    const int64_t q_ctas = std::min<int64_t>(a.hq, std::max<int64_t>(1, (a.hq * most + work / 2) / work));
+    a.kv_per = (int)((a.c.hkv + kv_ctas - 1) / kv_ctas);
+    a.q_per = a.hq > 0 ? (int)((a.hq + q_ctas - 1) / q_ctas) : 1;
+    a.kv_ctas = (a.c.hkv + a.kv_per - 1) / a.kv_per;
+    a.q_side = 1;
+    while (a.q_side * 2 <= std::min(a.q_per / rows_ahead<T>(), threads / (D / 16))) a.q_side *= 2;
+    const dim3 grid((unsigned)units, (unsigned)(a.kv_ctas + (a.hq + a.q_per - 1) / a.q_per));
+    return launch_with(cache_write_page_kernel<D, T, CT>, a, grid, threads, turns + 2 * (size_t)a.kv_per * sizeof(float),
+                       s);
+}
+
 template <int D, typename T>
-int launch_ct(const WriteArgs& a, int cache_dtype, dim3 grid, cudaStream_t s) {
-    return cache_dtype == LSA_E4M3 ? launch<D, T, uint8_t>(a, grid, s) : launch<D, T, __nv_bfloat16>(a, grid, s);
+int launch_ct(const WriteArgs& a, int cache_dtype, int64_t units, bool pages, cudaStream_t s) {
+    return cache_dtype == LSA_E4M3 ? launch<D, T, uint8_t>(a, units, pages, s)
+                                   : launch<D, T, __nv_bfloat16>(a, units, pages, s);
 }
 
 }  // namespace
@@ -329,18 +621,19 @@ int launch_cache_write(const lsa_kv_cache& cache, const void* K, const void* V, 
     const int64_t slots = n / cache.page + 2 * cache.batch;
     a.by_token = n < slots;
     const int64_t units = a.by_token ? n : slots;
-    const int rows = kWriteThreads / (cache.d / 16);
-    a.tokens_per_pass = 1;
-    while (a.tokens_per_pass < rows && a.tokens_per_pass < cache.page && a.tokens_per_pass * 2 * cache.batch <= n)
-        a.tokens_per_pass *= 2;
-    a.kv_per = cache.hkv;
-    a.q_per = hq;
-    const dim3 grid((unsigned)units, 1);
+    a.most_tokens = (int)std::min<int64_t>(cache.page, n);
+    a.lists = 2 * cache.hkv + hq;
+    // Whole pages are worth a kernel that reads them once when the sequences fill
+    // some, and when there is enough of it that reading twice leaves the caches
+    // (8-bit pages, 32 query and 4 KV heads of 128, few-token kernel and page kernel:
+    // 64 x 256 tokens in pages of 128 136 and 81 us, of 64 86.5 and 71.5, of 16 75.7
+    // and 67.8; 16 x 256 in pages of 16 18.7 and 25.6; 64 x 4 in pages of 64 6.1 and 8.9).
+    const bool pages = n >= cache.batch * cache.page && n * cache.page * cache.page >= (1 << 21);
     if (cache.d == 128)
-        return dtype == LSA_F32 ? launch_ct<128, float>(a, cache.dtype, grid, s)
-                                : launch_ct<128, __nv_bfloat16>(a, cache.dtype, grid, s);
-    return dtype == LSA_F32 ? launch_ct<64, float>(a, cache.dtype, grid, s)
-                            : launch_ct<64, __nv_bfloat16>(a, cache.dtype, grid, s);
+        return dtype == LSA_F32 ? launch_ct<128, float>(a, cache.dtype, units, pages, s)
+                                : launch_ct<128, __nv_bfloat16>(a, cache.dtype, units, pages, s);
+    return dtype == LSA_F32 ? launch_ct<64, float>(a, cache.dtype, units, pages, s)
+                            : launch_ct<64, __nv_bfloat16>(a, cache.dtype, units, pages, s);
 }
 
 }  // namespace lsa
