@@ -683,9 +683,12 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.dynamicSmemBytes = (size_t)kWarps * 2 * tiles_per_step<D, CT>() * 32 * D * sizeof(CT);
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CT, T, NT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
-    if (e != cudaSuccess) return cuda_status(e);
+    if (cfg.dynamicSmemBytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CT, T, NT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)cfg.dynamicSmemBytes);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = a.cluster;

@@ -565,8 +565,10 @@ __global__ __launch_bounds__(kMaxPageThreads) void cache_write_page_kernel(const
 
 template <typename K>
 int launch_with(K kernel, const WriteArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_status(e);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
     note_launch();
     kernel<<<grid, threads, smem, s>>>(a);
     return cuda_status(cudaGetLastError());

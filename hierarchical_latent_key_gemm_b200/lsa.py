@@ -632,10 +632,16 @@ def _io_code(t):
     return code
 
 
+def _current_stream_of(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without the Stream object (1.3 us a call)
+_current_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream_of)
+
+
 def _cache_stream(cache, stream):
-    if stream is None:
-        return torch.cuda.current_stream(cache.index).cuda_stream
-    return _stream(stream)
+    return _current_stream_of(cache.index) if stream is None else _stream(stream)
 
 
 def lsa_cache_write(cache: KVCache, K, V, cu, pos0, Q=None, inv_freq=None, interleaved=False, K_out=None, Q_out=None,

@@ -9,6 +9,8 @@ while the next chunk computes.  Every step moves all of Q, K, V and W up and
 all of O down; the overlap only hides the transfers behind the kernels.
 
 DecodeStep: decode with select + attention replayed from one CUDA graph.
+CachedDecodeStep: the same over a paged KV cache, the new token's rotation and
+write into the cache included.
 """
 from __future__ import annotations
 
@@ -150,5 +152,55 @@ class DecodeStep:
         lsa.lsa_append(self.index, self.K, 1)
         self.q.copy_(q_new)
         self.pos.fill_(pos)
+        self.graph.replay()
+        return self.O, self.lse
+
+
+class CachedDecodeStep:
+    """Decode steps over a paged KV cache, one new token per sequence: the
+    token's keys and values are written into the cache (keys and queries
+    rotated on the way) and indexed from its pages by plain calls, and select +
+    attention replay one CUDA graph captured at set-up.  The index was built
+    over the rotated keys of the tokens that are in the cache already; the
+    caller hands out pages by writing cache.page_table."""
+
+    def __init__(self, index, sp, cache, hq: int, max_sel: int, inv_freq=None, interleaved: bool = False):
+        p = index.params
+        self.dev = cache.K.device
+        self.index, self.sp, self.cache, self.max_sel = index, sp, cache, max_sel
+        self.inv_freq, self.interleaved = inv_freq, interleaved
+        B, d = p.batch, p.d
+        dtype = torch.float32 if p.dtype == lsa.LSA_F32 else torch.bfloat16
+        self.q = torch.zeros((B, 1, hq, d), dtype=dtype, device=self.dev)
+        self.cu = torch.arange(B + 1, dtype=torch.int64, device=self.dev)
+        self.pos = torch.full((B, 1), max(0, p.n_tokens - 1), dtype=torch.int64, device=self.dev)
+        self.idx = torch.empty((B, 1, p.hkv, max_sel), dtype=torch.int32, device=self.dev)
+        self.cnt = torch.empty((B, 1, p.hkv), dtype=torch.int32, device=self.dev)
+        self.O = torch.empty((B, 1, hq, d), dtype=dtype, device=self.dev)
+        self.lse = torch.empty((B, 1, hq), dtype=torch.float32, device=self.dev)
+        side = torch.cuda.Stream(self.dev)
+        side.wait_stream(torch.cuda.current_stream(self.dev))
+        with torch.cuda.stream(side):
+            self._select_attend()          # eager once: kernel attributes, scratch pool
+        torch.cuda.current_stream(self.dev).wait_stream(side)
+        torch.cuda.synchronize(self.dev)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph, stream=side):
+            self._select_attend()
+
+    def _select_attend(self):
+        lsa.lsa_select(self.index, self.sp, self.q, q_pos=self.pos, idx=self.idx, cnt=self.cnt,
+                       max_sel=self.max_sel)
+        lsa.lsa_cache_attn(self.cache, self.q, self.idx, self.cnt, O=self.O, lse=self.lse)
+
+    def step(self, k_new, v_new, q_new, pos: int):
+        """Write, index, select and attend the tokens at `pos`: k_new, v_new
+        [batch, hkv, d] and q_new [batch, hq, d], not rotated yet, of the
+        index's dtype; returns (O, lse) buffers that the next step overwrites."""
+        B, _, hq, d = self.q.shape
+        self.pos.fill_(pos)
+        lsa.lsa_cache_write(self.cache, k_new, v_new, self.cu, self.pos.view(B), Q=q_new, inv_freq=self.inv_freq,
+                            interleaved=self.interleaved, Q_out=self.q.view(B, hq, d))
+        lsa.lsa_append_cached(self.index, self.cache, 1)
         self.graph.replay()
         return self.O, self.lse

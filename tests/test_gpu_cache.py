@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import oracle as O
-from hierarchical_latent_key_gemm_b200 import lsa
+from hierarchical_latent_key_gemm_b200 import lsa, pipeline
 
 pytestmark = pytest.mark.gpu
 
@@ -649,3 +649,107 @@ def test_append_cached_latches_missing_pages():
     with pytest.raises(lsa.LsaError):           # past the append capacity
         lsa.lsa_append_cached(ix, cache, 13)
     ix.free()
+
+
+def test_decode_steps_replayed_from_a_graph_match_plain_calls():
+    """pipeline.CachedDecodeStep against the same calls made one by one on a second index and cache: the same bits at
+    every step."""
+    n0, steps, hkv, hq, d, pool, sink, window, topk = 1000, 12, 2, 8, 64, 4, 8, 64, 128
+    dev, f = "cuda", _inv_freq(d)
+    K, V, Q, _ = _served(E4, n0=n0, steps=steps)
+    sides = []
+    for _ in range(2):
+        cache = _shuffled_cache(2, n0 + steps, hkv, d, 32, E4, 5)
+        flat = lambda t, a, b: t[:, a:b].reshape(-1, t.shape[2], d).contiguous()
+        cu = torch.tensor([0, n0, 2 * n0], dtype=torch.int64, device=dev)
+        _, k = lsa.lsa_cache_write(cache, flat(K, 0, n0), flat(V, 0, n0), cu, torch.zeros(2, dtype=torch.int64,
+                                   device=dev), inv_freq=f, want_K=True)
+        dense = torch.zeros(2, n0 + steps, hkv, d, dtype=BF, device=dev)
+        dense[:, :n0] = k.view(2, n0, hkv, d)
+        bp = lsa.make_build_params(2, n0, n0 + steps, hkv, d, 32, pool, lsa.LSA_BF16, (8, 32), 3, 0, sink, steps)
+        ix = lsa.lsa_build_index(bp, dense, torch.eye(d, device=dev)[:, :32].contiguous())
+        sides.append((ix, cache))
+    sp = lsa.make_select_params(hq, 16, topk, sink, window)
+    max_sel = topk + sink + window
+    step = pipeline.CachedDecodeStep(sides[0][0], sp, sides[0][1], hq, max_sel, inv_freq=f)
+    one = torch.arange(3, dtype=torch.int64, device=dev)
+    for i in range(n0, n0 + steps):
+        k, v, q = flat(K, i, i + 1), flat(V, i, i + 1), flat(Q, i, i + 1)
+        got = [t.clone() for t in step.step(k, v, q, i)]
+        ix, cache = sides[1]
+        qr, _ = lsa.lsa_cache_write(cache, k, v, one, torch.full((2,), i, dtype=torch.int64, device=dev), Q=q,
+                                    inv_freq=f)
+        lsa.lsa_append_cached(ix, cache, 1)
+        idx, cnt = lsa.lsa_select(ix, sp, qr.view(2, 1, hq, d), q_pos0=i)
+        want = lsa.lsa_cache_attn(cache, qr.view(2, 1, hq, d), idx, cnt)
+        assert torch.equal(step.idx, idx) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert lsa.lsa_check(sides[0][0]) == lsa.lsa_check() == lsa.LSA_OK
+    for ix, _ in sides:
+        ix.free()
+
+
+@pytest.mark.parametrize("page,d,io,dtype,rot,inter", [
+    (16, 64, BF, E4, 64, False), (16, 128, F32, BF, 48, True), (32, 128, BF, BF, 80, True), (64, 64, F32, E4, 16, True),
+    (64, 128, BF, E4, 128, False), (128, 64, BF, E4, 32, True), (128, 128, F32, E4, 96, False),
+    (128, 128, BF, BF, 0, False), (32, 64, F32, BF, 64, False)])
+def test_write_of_long_chunks(page, d, io, dtype, rot, inter):
+    """Chunks of many pages (the kernel for whole pages), starting inside a page whose scale then grows, several KV
+    heads per CTA, query heads that do not fill a group, one sequence without a token."""
+    lens, pos0 = [2 * page + 2 ** 21 // page ** 2, 0, 3 * page + 5, 1], [page - 3, 7, 2 * page, 5 * page - 1]
+    cache = _shuffled_cache(4, max(lens) + max(pos0) + page, 3, d, page, dtype, 11)
+    if cache.scaled:
+        for name in "KV":
+            p = getattr(cache, name).view(torch.uint8)
+            p.copy_(torch.where((p & 0x7f) == 0x7f, p & 0x80, p))
+            getattr(cache, name + "_scale").fill_(2.0 ** -12)
+    before = _snapshot(cache)
+    K, V, Q, cu = _new_tokens(lens, 3, 15, d, io, 12, pad=2)
+    pos = torch.tensor(pos0, dtype=torch.int64, device="cuda")
+    K_out, Q_out = torch.zeros_like(K), torch.zeros_like(Q)
+    lsa.lsa_cache_write(cache, K, V, cu, pos, Q=Q, inv_freq=_inv_freq(rot), interleaved=inter, K_out=K_out, Q_out=Q_out)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    _check_write(cache, before, K, V, Q, K_out, Q_out, cu, pos, rot, inter)
+    assert torch.all(K_out[sum(lens):] == 0) and torch.all(Q_out[sum(lens):] == 0)
+    # the same into other pages, in place and without queries
+    twin = _shuffled_cache(4, max(lens) + max(pos0) + page, 3, d, page, dtype, 11)
+    for a, b in (("K", before["K_codes"]), ("V", before["V_codes"])):
+        getattr(twin, a).view(torch.uint8).copy_(b.view(torch.uint8))
+        if twin.scaled:
+            getattr(twin, a + "_scale").fill_(2.0 ** -12)
+    k = K.clone()
+    lsa.lsa_cache_write(twin, k, V, cu, pos, inv_freq=_inv_freq(rot), interleaved=inter, K_out=k)
+    n = sum(lens)
+    assert torch.equal(k[:n], K_out[:n])
+    assert torch.equal(twin.K.view(torch.uint8), cache.K.view(torch.uint8))
+    assert torch.equal(twin.V.view(torch.uint8), cache.V.view(torch.uint8))
+
+
+@pytest.mark.parametrize("io,dtype,d,G", [(BF, E4, 128, 8), (BF, BF, 64, 16), (F32, E4, 64, 3), (BF, E4, 64, 1)])
+def test_many_short_rows_take_whole_row_warps(io, dtype, d, G):
+    """Enough short rows that every warp takes whole ones, an odd number of them; against the same rows a few at a
+    time, which CTAs share."""
+    nq, hkv = 2501, 3
+    c = _filled(1, 400, hkv, d, 32, dtype, 95)
+    Q = torch.randn(1, nq, hkv * G, d, generator=_gen(96), device="cuda").to(io)
+    idx, cnt = _selection(np.random.RandomState(97), 1, nq, hkv, 50, 400, [50, 0, 1, 17, 33])
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    pick = torch.cat([torch.arange(0, 20), torch.arange(1230, 1240), torch.arange(nq - 20, nq)]).cuda()
+    few = [t[:, pick].contiguous() for t in (Q, idx, cnt, Oo, lse)]
+    _check_attn(c, *few)
+    o2, l2 = lsa.lsa_cache_attn(c, *few[:3])
+    # the same sums in another order: fp32 roundings of some 50 terms, then the output's
+    tol = {BF: 2.0 ** -7, F32: 2.0 ** -16}[io]
+    assert torch.all((o2.float() - few[3].float()).abs() <= tol * few[3].float().abs() + 2.0 ** -12)
+    assert torch.equal(torch.isinf(l2), torch.isinf(few[4]))
+
+
+def test_a_long_row_over_a_cluster():
+    """One row of 100,003 tokens shared by a cluster of CTAs."""
+    c = _filled(1, 131_072, 1, 128, 128, E4, 98)
+    for G, io in ((1, BF), (16, BF), (4, F32)):
+        Q = torch.randn(1, 1, G, 128, generator=_gen(99), device="cuda").to(io)
+        idx, cnt = _selection(np.random.RandomState(98), 1, 1, 1, 100_003, 131_072, [100_003])
+        Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+        assert lsa.lsa_check() == lsa.LSA_OK
+        _check_attn(c, Q, idx, cnt, Oo, lse)
