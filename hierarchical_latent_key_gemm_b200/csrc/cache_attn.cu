@@ -24,6 +24,8 @@
 // a fixed order.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "cache_common.cuh"
 #include "warp_mma.cuh"
 
@@ -34,7 +36,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 // Weights are at most 2^(kHeadroom + kLazy) and the largest at least 2^kHeadroom:
 // the maximum is renewed only when a score passes it by 2^kLazy.  In fp16 a
 // weight keeps 11 bits down to 2^-(14 + kHeadroom) of the largest, and what lies
@@ -649,11 +651,42 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
+template <int D, typename CT>
+constexpr size_t ring_bytes() { return (size_t)kWarps * 2 * tiles_per_step<D, CT>() * 32 * D * sizeof(CT); }
+
+// How many clusters of `size` CTAs the current device runs at once (a property of
+// the kernel and the device, asked for once); 0 where it cannot.
+template <int D, typename CT, typename T, int NT>
+int resident(int size) {
+    static std::atomic<int> known[128][5];            // + 1
+    int dev = 0, lg = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+    while ((1 << lg) < size) ++lg;
+    int n = known[dev][lg].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    const auto kernel = cache_attn_kernel<D, CT, T, NT>;
+    n = 0;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes<D, CT>());
+    if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = ring_bytes<D, CT>();
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = size;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    known[dev][lg].store(n + 1, std::memory_order_relaxed);
+    return n;
 }
 
 template <int D, typename CT, typename T, int NT>
@@ -663,37 +696,33 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     a.units = (uint32_t)units;
     const int step = 16 * tiles_per_step<D, CT>();
     const int64_t steps = (a.max_sel + step - 1) / step;
-    const int64_t resident = (int64_t)min_ctas<D, CT, T, NT>() * sm_count();
-    // Few rows: a cluster of CTAs shares each, while all of them fit on the GPU at
-    // once and every warp has a step (4 rows of 4,160 tokens, 16 heads of 128:
-    // 10.5 us with 8 CTAs a row, 33 with one; 128 rows of 1,600: 10.2 with 2, 12.4
-    // with one, 13.6 with 4).
+    const int64_t ctas = resident<D, CT, T, NT>(1);
+    if (ctas < 1) return LSA_ERR_CUDA;
+    // Few rows: a cluster of CTAs shares each, while all of them run at once and
+    // every warp has a step (4 rows of 4,160 tokens, 16 heads of 128: 8.8 us with 16
+    // CTAs a row, 10.5 with 8, 16.7 with 4; 128 rows of 1,600: 10.2 with 2, 13.2 with
+    // one, 14.4 with 4).
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && units * a.cluster * 2 <= resident && a.cluster * 2 * kWarps <= steps) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && a.cluster * 2 * kWarps <= steps &&
+           units <= resident<D, CT, T, NT>(a.cluster * 2))
+        a.cluster *= 2;
     // Many rows: a warp takes a whole one, which needs no merge, unless the last
     // round of warps would then run long.  In microseconds a CTA that shares a row
     // takes about 4 + steps / 4, four whole rows side by side 6 + steps (8 heads of
     // 128, 8-bit pages; 4,096 rows of 64 tokens: 41 us shared, 22 whole; 16,384 of
     // 512: 320 and 247; 1,024 of 2,048: 64 and 73).
-    const int64_t shared = (units + resident - 1) / resident * (4 + (steps + kWarps - 1) / kWarps);
-    const int64_t whole = (units + kWarps * resident - 1) / (kWarps * resident) * (6 + steps);
+    const int64_t shared = (units + ctas - 1) / ctas * (4 + (steps + kWarps - 1) / kWarps);
+    const int64_t whole = (units + kWarps * ctas - 1) / (kWarps * ctas) * (6 + steps);
     a.warps = a.cluster == 1 && whole < shared ? 1 : kWarps;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.warps == 1 ? (units + kWarps - 1) / kWarps : units * a.cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cfg.dynamicSmemBytes = (size_t)kWarps * 2 * tiles_per_step<D, CT>() * 32 * D * sizeof(CT);
-    if (cfg.dynamicSmemBytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, CT, T, NT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)cfg.dynamicSmemBytes);
-        if (e != cudaSuccess) return cuda_status(e);
-    }
+    cfg.dynamicSmemBytes = ring_bytes<D, CT>();
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = a.cluster;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     note_launch();
