@@ -123,28 +123,33 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, const uint32_t*
 }
 
 // Byte offset of 16-byte piece `i` of row r in a tile of rows of ROWB bytes:
-// permuted so that both the K pieces (8 rows, 4 neighbouring pieces) and the V
-// pieces (4 rows two apart, all pieces) of a warp's fragments hit 32 banks.
+// permuted so that neither a warp's K loads (8 rows, 4 neighbouring pieces) nor
+// its V loads (one piece of 8 rows) meet in a bank.
 template <int ROWB>
 __device__ __forceinline__ int piece_at(int r, int i) {
     if constexpr (ROWB == 64) {
         const int line = r >> 1;
-        return line * 128 + ((((r & 1) * 4 + i) ^ ((line & 3) << 1)) << 4);
+        return line * 128 + ((((r & 1) * 4 + i) ^ (line & 3)) << 4);
     } else {
         const int s = ((r & 1) << 2) | ((r >> 1) & 3);
         return r * ROWB + (((i & ~7) | ((i & 7) ^ s)) << 4);
     }
 }
 
-template <int N>
 __device__ __forceinline__ void load_shared(uint32_t p, uint32_t* w) {
-    if constexpr (N == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p) : "memory");
-    else
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(p)
-                     : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(p)
+                 : "memory");
+}
+// Two 16 x 16 byte matrices, transposed (lanes 0-15 and 16-31 hold the addresses
+// of their rows): bytes 4t .. 4t + 3 of w[0] are rows 4t .. 4t + 3 of column g of
+// the first, w[1] its column g + 8, w[2] and w[3] the second (lane = 4 g + t).
+__device__ __forceinline__ void load_transposed(uint32_t p, uint32_t* w) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(p)
+                 : "memory");
 }
 
 // piece_at(i * 32 / PIECES + r, p) = (piece_at(r, p) ^ step_swizzle(i)) + i * (32 / PIECES) * ROWB
@@ -152,19 +157,6 @@ template <int ROWB>
 __device__ __forceinline__ constexpr uint32_t step_swizzle(int i) {
     return ROWB == 64 ? 0u : ROWB == 128 ? (i & 1) << 5 : (i & 3) << 4;
 }
-
-// Which pair of components m tile i of thread g is: its V pieces are vp(g) (and
-// vp(g) + 8 of rows of 16 pieces), 8 bytes each of rows of 4 pieces.
-template <int D, int BYTES>
-__device__ __forceinline__ int pair_of(int i, int g) {
-    if constexpr (D * BYTES == 64) return 4 * g + i;
-    const int vp = (g & 1) * 4 + (g >> 1);
-    if constexpr (BYTES == 1) return 8 * vp + i;
-    return (i / 4) * 32 + 4 * vp + (i & 3);
-}
-// Where pair q of a head stands in the merge buffer: permuted so that neither
-// the fragments' writes nor the reads in order meet in a bank (two writes do).
-__device__ __forceinline__ int pair_at(int q) { return 2 * ((q & ~7) | ((q ^ (q >> 3)) & 7)); }
 
 __device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 __device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
@@ -193,13 +185,12 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     constexpr int HG = 8 * NT;                        // heads of a warp
     constexpr int ROWB = D * (int)sizeof(CT);         // bytes of a row
     constexpr int KW = ROWB / 16;                     // words of a K row in a thread (4 threads a row)
-    constexpr int VW = ROWB / 32;                     // words of a V row in a thread (8 threads a row)
     constexpr int PIECES = ROWB / 16;
     constexpr int TILE = 16 * ROWB;                   // bytes of 16 rows
     constexpr int TPS = tiles_per_step<D, CT>();
     constexpr int STEP = 16 * TPS;                    // tokens of a warp's step
     constexpr int BUFFER = TPS * 2 * TILE;            // bytes of a step: (K tile, V tile) TPS times
-    constexpr int LD = D + 2;                         // row stride of the merge buffers
+    constexpr int LD = D + 4;                         // row stride of the merge buffers
     extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][2][BUFFER]; at the end [HG][LD] of a warp
     __shared__ float m_s[kWarps][HG], l_s[kWarps][HG];
     // what the CTAs of a cluster send: a share of the sums, and all maxima and sums of weights
@@ -209,6 +200,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     const CacheArgs& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    // Rows g and g + 8 of a K tile are tokens krow and krow + KROW of its 16: the order in which the transposed loads
+    // of V rows bring the tokens (8-bit: 4t, 4t + 1, then 4t + 2, 4t + 3; bf16: 2t, 2t + 1, then 2t + 8, 2t + 9)
+    constexpr int KROW = E4 ? 2 : 8;
+    const int krow = E4 ? 4 * (g >> 1) + (g & 1) : g;
     const int rank = blockIdx.x % a.cluster;
     if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // all have started: waited for below
     const bool alone = a.warps == 1;                  // a warp takes a whole row
@@ -369,12 +364,18 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
     }
 
-    // shared addresses of this thread's pieces: K pieces t + 4 i of rows g + 8 e, V pieces vp + 8 i of rows
-    // 2t + (e & 1) + 8 (e >> 1)
-    const int vp = (g & 1) * (PIECES < 8 ? 0 : 4) + (g >> 1);
-    uint32_t k0 = ring + piece_at<ROWB>(g, t), k1 = ring + piece_at<ROWB>(g, t + (PIECES < 8 ? 0 : 4));
-    uint32_t v0 = ring + piece_at<ROWB>(2 * t, vp) + (VW == 2 ? 8 * (g & 1) : 0);
-    uint32_t v1 = ring + piece_at<ROWB>(2 * t + 1, vp) + (VW == 2 ? 8 * (g & 1) : 0);
+    // shared addresses: K pieces t and t + 4 of rows krow and krow + KROW (they differ in bits that the permutation
+    // of piece_at changes), and this lane's rows of the V tile's transposed loads
+    uint32_t kp[2][2], vp[ROWB / 32 > 4 ? 4 : ROWB / 32];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            kp[e][i] = ring + piece_at<ROWB>(krow + KROW * e, t + (PIECES < 8 ? 0 : 4 * i));
+    const int vrow = E4 ? lane & 15 : (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(vp) / 4); ++i)
+        vp[i] = ring + TILE + piece_at<ROWB>(vrow, 2 * i + (E4 ? lane >> 4 : lane >> 3 & 1));
     uint32_t ahead = ring + BUFFER;
     int32_t flip = BUFFER;
     for (; step < steps; step += stride) {
@@ -400,8 +401,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int i = 0; i < KW / 4; ++i)
-                    load_shared<4>((i & 1 ? k1 : k0) + (half * 2 * TILE + 8 * e * ROWB + 128 * (i / 2)),
-                                   kr[e] + 4 * i);
+                    load_shared(kp[e][i & 1] + (half * 2 * TILE + 128 * (i / 2)), kr[e] + 4 * i);
             float z[NT][4];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -440,9 +440,9 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 float ks = 1.f, lv = 0.f;
                 iv[half][e] = 1.f;
                 if (E4) {
-                    ks = __shfl_sync(0xffffffffu, cur.ks, 16 * half + g + 8 * e);
-                    lv = __shfl_sync(0xffffffffu, lg, 16 * half + g + 8 * e);
-                    iv[half][e] = __shfl_sync(0xffffffffu, inv, 16 * half + g + 8 * e);
+                    ks = __shfl_sync(0xffffffffu, cur.ks, 16 * half + krow + KROW * e);
+                    lv = __shfl_sync(0xffffffffu, lg, 16 * half + krow + KROW * e);
+                    iv[half][e] = __shfl_sync(0xffffffffu, inv, 16 * half + krow + KROW * e);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!(cur.ok >> (16 * half + g + 8 * (e >> 1)) & 1u)) y[half][nt][e] = -INFINITY;
+                        if (!(cur.ok >> (16 * half + krow + KROW * (e >> 1)) & 1u)) y[half][nt][e] = -INFINITY;
             top = INFINITY;            // maxima of what is left
         }
         if (__any_sync(0xffffffffu, top > kHeadroom + kLazy || any_unset)) {
@@ -498,17 +498,6 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
         }
 #pragma unroll
         for (int half = 0; half < TPS; ++half) {
-            uint32_t vr[4][VW];        // rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t p = (e & 1 ? v1 : v0) + (half * 2 * TILE + TILE + 8 * (e >> 1) * ROWB);
-                if constexpr (VW == 2) {
-                    load_shared<2>(p, vr[e]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VW / 4; ++i) load_shared<4>(p + 128 * i, vr[e] + 4 * i);
-                }
-            }
             // ---- weights: B fragments of P^T
             uint32_t pb[PP][NT][2];
 #pragma unroll
@@ -528,33 +517,40 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     pb[p][nt][1] = movmatrix_t(hi[p]);
                 }
             }
-            // ---- acc: rows g and g + 8 of m tile i are component(i, g) and the next
+            // ---- acc: rows g and g + 8 of m tile i are components 16 i + g and 16 i + g + 8
 #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                uint32_t va[4];
+            for (int i = 0; i < KS; i += E4 ? 2 : 1) {
+                uint32_t va[2][4];
+                // 32 bytes of every row: of 256-byte rows the second 128 are a fixed distance on
+                constexpr int NV = (int)(sizeof(vp) / 4);
+                const int j = E4 ? i / 2 : i;
+                const uint32_t p = vp[j % NV] + (half * 2 * TILE + 128 * (j / NV));
+                if constexpr (E4) {
+                    uint32_t w[4];
+                    load_transposed(p, w);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {       // tokens 2t, 2t + 1, then 2t + 8, 2t + 9
-                    if constexpr (E4) {
-                        e4m3x4_to_f16x4(__byte_perm(vr[2 * e][i / 2], vr[2 * e + 1][i / 2], i % 2 ? 0x7362 : 0x5140),
-                                        va[2 * e], va[2 * e + 1]);
-                    } else {
-                        va[2 * e] = __byte_perm(vr[2 * e][i], vr[2 * e + 1][i], 0x5410);
-                        va[2 * e + 1] = __byte_perm(vr[2 * e][i], vr[2 * e + 1][i], 0x7632);
+                    for (int x = 0; x < 2; ++x) {
+                        e4m3x4_to_f16x4(w[2 * x], va[x][0], va[x][2]);
+                        e4m3x4_to_f16x4(w[2 * x + 1], va[x][1], va[x][3]);
                     }
+                } else {
+                    ldsm_x4_t(p, va[0][0], va[0][1], va[0][2], va[0][3]);
                 }
 #pragma unroll
-                for (int p = 0; p < PP; ++p)
+                for (int x = 0; x < (E4 ? 2 : 1); ++x)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma<E4>(o[i][nt], va, pb[p][nt]);
+                    for (int q = 0; q < PP; ++q)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma<E4>(o[i + x][nt], va[x], pb[q][nt]);
             }
         }
         __syncwarp();          // the buffer is free
         cur = next;
         ahead -= flip;
-        k0 += flip;
-        k1 += flip;
-        v0 += flip;
-        v1 += flip;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kp[i / 2][i % 2] += flip;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(vp) / 4); ++i) vp[i] += flip;
         flip = -flip;
     }
     cp_async_wait<0>();
@@ -576,9 +572,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 l_s[warp][head] = s;
             }
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
-                *reinterpret_cast<float2*>(mine + head * LD + pair_at(pair_of<D, (int)sizeof(CT)>(i, g))) =
-                    make_float2(o[i][nt][e], o[i][nt][e + 2]);
+            for (int i = 0; i < KS; ++i) {
+                mine[head * LD + 16 * i + g] = o[i][nt][e];
+                mine[head * LD + 16 * i + 8 + g] = o[i][nt][e + 2];
+            }
         }
     if (alone) __syncwarp();
     else __syncthreads();
@@ -603,7 +600,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             if (w >= w0 && w < w1) {
-                const float2 v = *reinterpret_cast<const float2*>(part + w * (2 * BUFFER / 4) + pair_at(q));
+                const float2 v = *reinterpret_cast<const float2*>(part + w * (2 * BUFFER / 4) + 2 * q);
                 s.x += f[w] * v.x;
                 s.y += f[w] * v.y;
             }
