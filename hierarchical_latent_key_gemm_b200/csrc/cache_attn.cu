@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     // bytes a lane and copy; zeros where there is no token
     const uint32_t ring = smem_u32(ring_s) + warp * 2 * BUFFER;
     const unsigned char* Kc = static_cast<const unsigned char*>(c.K) + 16 * (lane % PIECES);
-    const int64_t k_to_v = static_cast<const unsigned char*>(c.V) - static_cast<const unsigned char*>(c.K);
+    const unsigned char* Vc = static_cast<const unsigned char*>(c.V) + 16 * (lane % PIECES);
     const uint32_t lane_at = piece_at<ROWB>(lane / PIECES, lane % PIECES);
     auto gather = [&](const Where& w, int half, uint32_t buffer) {
         constexpr int RP = 32 / PIECES;               // rows of a copy
@@ -289,21 +289,19 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
 #pragma unroll
             for (int i = 0; i < 16 / RP; ++i) {
                 const uint32_t at = __shfl_sync(0xffffffffu, w.row, 16 * half + i * RP + lane / PIECES);
-                const unsigned char* src = Kc + (uint64_t)at * ROWB;
                 const uint32_t dst = buffer + (lane_at ^ step_swizzle<ROWB>(i)) + (half * 2 * TILE + i * RP * ROWB);
-                cp_async16(dst, src);
-                cp_async16(dst + TILE, src + k_to_v);
+                cp_async16(dst, Kc + (uint64_t)at * ROWB);
+                cp_async16(dst + TILE, Vc + (uint64_t)at * ROWB);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 16 / RP; ++i) {
                 const int j = 16 * half + i * RP + lane / PIECES;
                 const uint32_t at = __shfl_sync(0xffffffffu, w.row, j);
-                const unsigned char* src = Kc + (uint64_t)at * ROWB;
                 const uint32_t dst = buffer + (lane_at ^ step_swizzle<ROWB>(i)) + (half * 2 * TILE + i * RP * ROWB);
                 const int bytes = w.ok >> j & 1u ? 16 : 0;
-                cp_async16(dst, src, bytes);
-                cp_async16(dst + TILE, src + k_to_v, bytes);
+                cp_async16(dst, Kc + (uint64_t)at * ROWB, bytes);
+                cp_async16(dst + TILE, Vc + (uint64_t)at * ROWB, bytes);
             }
         }
     };
