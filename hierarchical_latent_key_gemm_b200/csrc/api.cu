@@ -396,7 +396,7 @@ bool valid_cache(const lsa_kv_cache* c) {
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return false;
     if (c->dtype != LSA_BF16 && c->dtype != LSA_E4M3) return false;
     // page ids are int32; the last token of a row of the table stays within int32
-    if (c->n_pages > INT32_MAX || c->ld_pages > ((int64_t)1 << 31) / c->page || c->batch > 65535 || c->hkv > 4096)
+    if (c->n_pages > INT32_MAX || c->ld_pages > ((int64_t)1 << 31) / c->page || c->batch > 65535 || c->hkv > 1024)
         return false;
     if (c->n_pages * c->hkv * c->page >= 0xffffffffll) return false;   // rows of the pools are uint32
     if (!is_here(c->K) || !is_here(c->V) || !is_here(c->page_table)) return false;
@@ -593,7 +593,7 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
     if (!valid_cache(cache)) return LSA_ERR_INVALID_ARG;
     if (dtype != LSA_F32 && dtype != LSA_BF16) return LSA_ERR_INVALID_ARG;
     if (rot < 0 || rot > cache->d || rot % 16 || (rot > 0 && !is_here(inv_freq))) return LSA_ERR_INVALID_ARG;
-    if (n < 0 || n > INT32_MAX || hq < 0 || hq > 65535 || !is_here(cu) || !is_here(pos0))
+    if (n < 0 || n > INT32_MAX || hq < 0 || hq > 4096 || !is_here(cu) || !is_here(pos0))
         return LSA_ERR_INVALID_ARG;
     if (n == 0) return LSA_OK;
     if (!is_here(K) || !is_here(V) || !aligned16(K) || !aligned16(V)) return LSA_ERR_INVALID_ARG;
@@ -613,7 +613,7 @@ int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx,
     if (nq < 0 || nq > INT32_MAX || hq < cache->hkv || hq % cache->hkv || hq / cache->hkv > 64 || max_sel < 1)
         return LSA_ERR_INVALID_ARG;
     if (nq == 0) return LSA_OK;
-    if (cache->batch * nq * hq > INT32_MAX / 16) return LSA_ERR_INVALID_ARG;
+    if (cache->batch * nq * hq > INT32_MAX) return LSA_ERR_INVALID_ARG;
     if (!is_here(Q) || !is_here(idx) || !is_here(cnt) || !is_here(O) || !aligned16(Q) ||
         !aligned16(O))
         return LSA_ERR_INVALID_ARG;

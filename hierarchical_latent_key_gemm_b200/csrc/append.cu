@@ -61,19 +61,21 @@ template <typename CT>
 struct CachedKeys {
     CacheArgs c;
     __device__ float mean(const AppArgs& a, int64_t bseq, int64_t b, int h, int k) const {
-        return mean_of([&](int m) {
-            const int64_t tok = b * a.pool + m;
+        bool bad = false;
+        const float m = mean_of([&](int i) {
+            const int64_t tok = b * a.pool + i;
             const int pid = cache_page(c, bseq, tok);
-            if (pid < 0) {
-                latch(a.err, kErrDevice);
-                return 0.f;
-            }
-            const CT* p = static_cast<const CT*>(c.K) + cache_row(c, pid, h, tok) * a.d + k;
+            bad |= pid < 0;
+            const CT* p = static_cast<const CT*>(c.K) + (pid < 0 ? 0 : cache_row(c, pid, h, tok) * a.d) + k;
+            float x;
             if constexpr (sizeof(CT) == 1)
-                return e4m3x4_to_f32x4(*p).x * c.K_scale[(int64_t)pid * c.hkv + h];
+                x = e4m3x4_to_f32x4(*p).x * c.K_scale[pid < 0 ? 0 : (int64_t)pid * c.hkv + h];
             else
-                return to_f32(*p);
+                x = to_f32(*p);
+            return pid < 0 ? 0.f : x;
         }, a.pool);
+        if (bad) latch(a.err, kErrDevice);
+        return m;
     }
 };
 

@@ -11,13 +11,26 @@
 // of the exponent, and weights of pages with very different scales meet the
 // tensor cores at the size they contribute with.
 //
+// What bounds it.  The rows are scattered (whole rows of 64 to 256 bytes, pages
+// anywhere), each is used by the 4 to 16 heads of its group only, and a round of
+// gathers takes 1 to 1.7 us on this GPU even from L2: the rate is what is in
+// flight, so every warp keeps a step's rows (32 tokens, 8 KB) on their way to
+// shared memory by cp.async while it works on the step before, and looks the
+// rows of later steps up (token, page, scales) one load a step.  With that,
+// decode is bound by HBM (96 sequences, 32 heads of 128 over 4 KV heads, 2,624
+// rows of 8 bits: 47-51 us, 5.2-5.6 TB/s) and long chunks by instructions: the
+// conversion of the codes, two a cvt, on half the lanes of the ALU (2,048
+// queries x 16 heads, 3,136 rows: 311 us, 10.6 TB/s of rows, 169 TFLOP/s).
+//
 // A warp takes 16 tokens at a time on the M side of mma.sync m16n8k16 (keys x
-// heads, then components x heads), so 8 heads fill a tile without padding.
-// The sums over d and over tokens do not depend on their order: a thread's
-// fragments are therefore whole 16-byte pieces of the gathered rows, loaded
-// from the pages straight into registers in the order the tensor cores want
-// them, without shared memory.  8-bit codes become fp16 exactly; queries are
-// scaled by a power of two per head so that bf16 values are fp16 values too.
+// heads, then components x heads), so 8 heads fill a tile without padding; the
+// 128 rows of a tcgen05 tile would have 8 heads to share them with.  The sums
+// over d and over tokens do not depend on their order: a K fragment is whole
+// 16-byte pieces of a row, with the queries laid out to match, a V fragment one
+// transposed load, with the K rows' order to match.  8-bit codes become fp16
+// exactly; queries are scaled by a power of two per head so that bf16 values are
+// fp16 values too.  fp32 queries and weights go as two fp16 parts (three bf16
+// parts next to bf16 pages), so fp32 results keep fp32's accuracy.
 //
 // The warps of a CTA, and the CTAs of a cluster, take every n-th step of one
 // row; their (m, l, acc) are merged in shared and distributed shared memory in
@@ -329,7 +342,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             // largest component to [2^14, 2^15): fp16's subnormals begin 2^-28 below it
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = min(100, max(-100, 14 - ((__float_as_int(top) >> 23) - 127)));
+            const int e = min(100, 14 - ((__float_as_int(top) >> 23) - 127));    // -114 for an infinity
             up = __int_as_float((127 + e) << 23);
             down = __int_as_float((127 - e) << 23);
         }
@@ -694,9 +707,9 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     const int64_t ctas = resident<D, CT, T, NT>(1);
     if (ctas < 1) return LSA_ERR_CUDA;
     // Few rows: a cluster of CTAs shares each, while all of them run at once and
-    // every warp has a step (4 rows of 4,160 tokens, 16 heads of 128: 8.8 us with 16
-    // CTAs a row, 10.5 with 8, 16.7 with 4; 128 rows of 1,600: 10.2 with 2, 13.2 with
-    // one, 14.4 with 4).
+    // every warp has a step (4 rows of 4,160 tokens, 16 heads of 128, 8-bit pages:
+    // 8.7 us with 16 CTAs a row, 10.4 with 8, 14.5 with 4, 35 with one; 128 rows of up
+    // to 1,599, 4 heads of 64, bf16: 10.7 with 2, 12.5 with one, 15.0 with 4).
     a.cluster = 1;
     while (a.cluster < kMaxCluster && a.cluster * 2 * kWarps <= steps &&
            units <= resident<D, CT, T, NT>(a.cluster * 2))
@@ -704,8 +717,8 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     // Many rows: a warp takes a whole one, which needs no merge, unless the last
     // round of warps would then run long.  In microseconds a CTA that shares a row
     // takes about 4 + steps / 4, four whole rows side by side 6 + steps (8 heads of
-    // 128, 8-bit pages; 4,096 rows of 64 tokens: 41 us shared, 22 whole; 16,384 of
-    // 512: 320 and 247; 1,024 of 2,048: 64 and 73).
+    // 128, 8-bit pages; 4,096 rows of 64 tokens: 39 us shared, 21 whole; 16,384 of
+    // 512: 299 and 227; 1,024 of 2,048: 59 and 66).
     const int64_t shared = (units + ctas - 1) / ctas * (4 + (steps + kWarps - 1) / kWarps);
     const int64_t whole = (units + kWarps * ctas - 1) / (kWarps * ctas) * (6 + steps);
     a.warps = a.cluster == 1 && whole < shared ? 1 : kWarps;

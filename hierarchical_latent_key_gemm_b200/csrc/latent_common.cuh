@@ -14,6 +14,7 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 template <typename F>
 __device__ __forceinline__ float mean_of(const F& at, int M) {
     float s = 0.f;
+#pragma unroll 4
     for (int m = 0; m < M; ++m) s = __fadd_rn(s, at(m));
     return __fdiv_rn(s, (float)M);
 }

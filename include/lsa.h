@@ -412,7 +412,7 @@ typedef struct {
     int64_t batch;             /* sequences (rows of page_table) */
     int64_t ld_pages;          /* entries per page_table row */
     int32_t page;              /* tokens per page: 16, 32, 64 or 128 */
-    int32_t hkv;               /* KV heads */
+    int32_t hkv;               /* KV heads, at most 1024 */
     int32_t d;                 /* head dimension: 64 or 128 */
     int32_t dtype;             /* LSA_BF16 or LSA_E4M3 */
     void* K;                   /* device [n_pages][hkv][page][d], 16-byte aligned */
@@ -420,13 +420,13 @@ typedef struct {
     float* K_scale;            /* device [n_pages][hkv] (LSA_E4M3; ignored for LSA_BF16): */
     float* V_scale;            /*   value = code * scale, 2^-64 <= scale <= 2^64 */
     const int32_t* page_table; /* device [batch][ld_pages]: token t of sequence b is slot t % page of page
-                                  page_table[b][t / page]; entries of pages not yet given out are not read */
+                                  page_table[b][t / page]; pages not yet given out are named -1, or never reached */
 } lsa_kv_cache;
 
 /* Write new tokens' keys and values into the cache, with the position rotation
  * applied to the keys (and to the step's queries) on the way.
  *  K, V: device [n][hkv][d], Q: device [n][hq][d], all of dtype (LSA_F32 or
- *      LSA_BF16); Q may be NULL with hq = 0.  V is not rotated.
+ *      LSA_BF16), hq <= 4096; Q may be NULL with hq = 0.  V is not rotated.
  *  cu: device int64 [batch+1], ascending: rows cu[b] .. cu[b+1]-1 are the new
  *      tokens of sequence b, at positions pos0[b], pos0[b]+1, ... (device int64
  *      [batch]); pos0[b] tokens are in its pages already.  A sequence may bring
@@ -455,7 +455,8 @@ typedef struct {
  *  - Found on the device and latched as LSA_ERR_DEVICE: cu not ascending within
  *    [0, n] (nothing is written); a negative position, a position past the page
  *    table or a page id outside [0, n_pages) (that page's tokens are skipped).
- *  - No allocation, one kernel, no state kept: capturable. */
+ *  - No allocation, one kernel, no state kept: capturable (the library's first
+ *    call on a device belongs before a capture). */
 int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, const void* Q, int64_t n,
                     const int64_t* cu, const int64_t* pos0, int32_t hq, int32_t dtype, const double* inv_freq,
                     int32_t rot, int32_t interleaved, void* K_out, void* Q_out, void* stream);
@@ -471,7 +472,7 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
  * LSA_ERR_DEVICE.  Only the selected tokens are read, so what stale or empty
  * slots hold does not matter.  Sums, maxima and products are accumulated in
  * fp32; the same inputs give the same bits.  No allocation, one kernel:
- * capturable. */
+ * capturable (after a first call on the device outside a capture). */
 int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
                    int32_t hq, int32_t dtype, int32_t max_sel, void* O, float* lse, void* stream);
 

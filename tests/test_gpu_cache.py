@@ -405,6 +405,18 @@ def test_attention_with_large_scores_and_queries(io):
     Q = Q.to(io)
     Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
     _check_attn(c, Q, idx, cnt, Oo, lse)
+    # near the largest number: the largest score takes all the weight
+    Q.zero_()
+    Q[:, :, :, 3] = 1e37
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    k, v = _values(c, "K"), _values(c, "V")
+    table, rows = c.page_table[0].cpu().numpy(), idx[0, :, 0].cpu().numpy()
+    for i, n in enumerate(cnt[0, :, 0].tolist()):
+        t = rows[i, :n]
+        s = k[table[t // 16], 0, t % 16, 3]
+        top = v[table[t // 16], 0, t % 16][s == s.max()].mean(0)     # 8-bit keys tie
+        assert np.all(np.abs(Oo[0, i].double().cpu().numpy() - top) <= 2.0 ** -7 * np.abs(top) + 2.0 ** -20)
+        assert torch.isfinite(lse[0, i]).all()
 
 
 @pytest.mark.parametrize("io", [BF, F32])
