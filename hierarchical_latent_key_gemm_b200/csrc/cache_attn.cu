@@ -188,6 +188,17 @@ constexpr int min_ctas() {
 template <int D, typename CT>
 constexpr int tiles_per_step() { return D * sizeof(CT) <= 128 ? 2 : 1; }
 
+// c += a b, the product apart: the tensor cores cut a running sum off at 24 bits
+// without rounding, which over a long row costs fp32 results a few bits; rounded
+// additions do not (rows of 3,000: 9e-6 off with sums kept in the tensor cores).
+template <bool F16>
+__device__ __forceinline__ void mma_added(float* c, const uint32_t* a, const uint32_t* b) {
+    float p[4];
+    mma_first<F16>(p, a, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] += p[e];
+}
+
 template <int D, typename CT, typename T, int NT>
 __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_attn_kernel(const AttnArgs a) {
     constexpr bool E4 = sizeof(CT) == 1;              // 8-bit codes, fp16 products; else bf16
@@ -432,6 +443,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     for (int nt = 0; nt < NT; ++nt) {
                         float* acc = (s & 1) ? z[nt] : y[half][nt];
                         if (s < 2 && p == 0) mma_first<E4>(acc, ka, qf[p][s][nt]);
+                        else if constexpr (F32) mma_added<E4>(acc, ka, qf[p][s][nt]);
                         else mma<E4>(acc, ka, qf[p][s][nt]);
                     }
             }
@@ -552,7 +564,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
 #pragma unroll
                     for (int q = 0; q < PP; ++q)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma<E4>(o[i + x][nt], va[x], pb[q][nt]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (F32) mma_added<E4>(o[i + x][nt], va[x], pb[q][nt]);
+                            else mma<E4>(o[i + x][nt], va[x], pb[q][nt]);
+                        }
             }
         }
         __syncwarp();          // the buffer is free
