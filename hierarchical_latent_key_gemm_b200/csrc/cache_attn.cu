@@ -188,24 +188,19 @@ constexpr int min_ctas() {
 template <int D, typename CT>
 constexpr int tiles_per_step() { return D * sizeof(CT) <= 128 ? 2 : 1; }
 
-// c += a b, the product apart: the tensor cores cut a running sum off at 24 bits
-// without rounding, which over a long row costs fp32 results a few bits; rounded
-// additions do not (rows of 3,000: 9e-6 off with sums kept in the tensor cores).
-template <bool F16>
-__device__ __forceinline__ void mma_added(float* c, const uint32_t* a, const uint32_t* b) {
-    float p[4];
-    mma_first<F16>(p, a, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] += p[e];
-}
-
 template <int D, typename CT, typename T, int NT>
 __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_attn_kernel(const AttnArgs a) {
     constexpr bool E4 = sizeof(CT) == 1;              // 8-bit codes, fp16 products; else bf16
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int PQ = F32 ? (E4 ? 2 : 3) : 1;        // 16-bit parts of a query component
     constexpr int PP = F32 ? (E4 ? 2 : 3) : (E4 ? 1 : 2);   // and of a weight
+    // The tensor cores cut a running sum off at 24 bits without rounding.  For fp32
+    // results sums are therefore kept outside, by rounded additions: every product of
+    // a score, every step of acc (with sums in the tensor cores 7.7e-7 off the exact
+    // result on the median, 4.9e-7 so; of rows of 2,000 to 3,000 up to 9e-6).
+    constexpr bool SUMS = F32;
     constexpr int KS = D / 16;                        // k steps of K Q^T, m tiles of V^T P^T
+    constexpr int MV = E4 ? 2 : 1;                    // m tiles of a V load
     constexpr int HG = 8 * NT;                        // heads of a warp
     constexpr int ROWB = D * (int)sizeof(CT);         // bytes of a row
     constexpr int KW = ROWB / 16;                     // words of a K row in a thread (4 threads a row)
@@ -443,8 +438,13 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     for (int nt = 0; nt < NT; ++nt) {
                         float* acc = (s & 1) ? z[nt] : y[half][nt];
                         if (s < 2 && p == 0) mma_first<E4>(acc, ka, qf[p][s][nt]);
-                        else if constexpr (F32) mma_added<E4>(acc, ka, qf[p][s][nt]);
-                        else mma<E4>(acc, ka, qf[p][s][nt]);
+                        else if constexpr (!SUMS) mma<E4>(acc, ka, qf[p][s][nt]);
+                        else {
+                            float sum[4];
+                            mma_first<E4>(sum, ka, qf[p][s][nt]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[e] += sum[e];
+                        }
                     }
             }
 #pragma unroll
@@ -519,10 +519,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     }
                 }
         }
+        // ---- weights: B fragments of P^T
+        uint32_t pb[TPS][PP][NT][2];
 #pragma unroll
-        for (int half = 0; half < TPS; ++half) {
-            // ---- weights: B fragments of P^T
-            uint32_t pb[PP][NT][2];
+        for (int half = 0; half < TPS; ++half)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
@@ -536,23 +536,26 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                 split<E4, PP>(w[2], w[3], hi);
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
-                    pb[p][nt][0] = movmatrix_t(lo[p]);
-                    pb[p][nt][1] = movmatrix_t(hi[p]);
+                    pb[half][p][nt][0] = movmatrix_t(lo[p]);
+                    pb[half][p][nt][1] = movmatrix_t(hi[p]);
                 }
             }
-            // ---- acc: rows g and g + 8 of m tile i are components 16 i + g and 16 i + g + 8
+        // ---- acc: rows g and g + 8 of m tile i are components 16 i + g and 16 i + g + 8
 #pragma unroll
-            for (int i = 0; i < KS; i += E4 ? 2 : 1) {
-                uint32_t va[2][4];
+        for (int i = 0; i < KS; i += MV) {
+            float sum[MV][NT][4];      // of this step (fp32, see SUMS)
+#pragma unroll
+            for (int half = 0; half < TPS; ++half) {
+                uint32_t va[MV][4];
                 // 32 bytes of every row: of 256-byte rows the second 128 are a fixed distance on
                 constexpr int NV = (int)(sizeof(vp) / 4);
-                const int j = E4 ? i / 2 : i;
+                const int j = i / MV;
                 const uint32_t p = vp[j % NV] + (half * 2 * TILE + 128 * (j / NV));
                 if constexpr (E4) {
                     uint32_t w[4];
                     load_transposed(p, w);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < MV; ++x) {
                         e4m3x4_to_f16x4(w[2 * x], va[x][0], va[x][2]);
                         e4m3x4_to_f16x4(w[2 * x + 1], va[x][1], va[x][3]);
                     }
@@ -560,15 +563,23 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     ldsm_x4_t(p, va[0][0], va[0][1], va[0][2], va[0][3]);
                 }
 #pragma unroll
-                for (int x = 0; x < (E4 ? 2 : 1); ++x)
+                for (int x = 0; x < MV; ++x)
 #pragma unroll
                     for (int q = 0; q < PP; ++q)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (F32) mma_added<E4>(o[i + x][nt], va[x], pb[q][nt]);
-                            else mma<E4>(o[i + x][nt], va[x], pb[q][nt]);
+                            if constexpr (!SUMS) mma<E4>(o[i + x][nt], va[x], pb[half][q][nt]);
+                            else if (half == 0 && q == 0) mma_first<E4>(sum[x][nt], va[x], pb[half][q][nt]);
+                            else mma<E4>(sum[x][nt], va[x], pb[half][q][nt]);
                         }
             }
+            if constexpr (SUMS)
+#pragma unroll
+                for (int x = 0; x < MV; ++x)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i + x][nt][e] += sum[x][nt][e];
         }
         __syncwarp();          // the buffer is free
         cur = next;
