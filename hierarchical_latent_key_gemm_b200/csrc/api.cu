@@ -378,20 +378,28 @@ bool attn_aligned(int dtype, const void* Q, const void* K, const void* V, const 
 
 // Memory of the current device (or managed): a call for a cache of another
 // device must fail here, not on the GPU.
-bool is_here(const void* p) {
-    cudaPointerAttributes at;
-    int dev = 0;
-    if (!p || cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
+struct Here {
+    int dev = -1;
+    Here() {
+        if (cudaGetDevice(&dev) != cudaSuccess) {
+            cudaGetLastError();
+            dev = -1;
+        }
     }
-    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
-}
+    bool operator()(const void* p) const {
+        cudaPointerAttributes at;
+        if (!p || cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+    }
+};
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A cache's own description; the attention and the append only read it.
-bool valid_cache(const lsa_kv_cache* c) {
+bool valid_cache(const lsa_kv_cache* c, const Here& is_here) {
     if (!c || c->batch < 1 || c->n_pages < 1 || c->ld_pages < 1 || c->hkv < 1 || !valid_d(c->d)) return false;
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return false;
     if (c->dtype != LSA_BF16 && c->dtype != LSA_E4M3) return false;
@@ -579,9 +587,11 @@ int lsa_append(lsa_index* index, const void* K, int64_t n_new, void* stream) {
 }
 
 int lsa_append_cached(lsa_index* index, const lsa_kv_cache* cache, int64_t n_new, void* stream) {
-    if (!live(index) || n_new < 0 || !valid_cache(cache)) return LSA_ERR_INVALID_ARG;
+    const Here is_here;
+    if (!live(index) || n_new < 0 || !valid_cache(cache, is_here)) return LSA_ERR_INVALID_ARG;
     const lsa_build_params& p = index->p;
-    if (cache->batch != p.batch || cache->hkv != p.hkv || cache->d != p.d) return LSA_ERR_INVALID_ARG;
+    if (cache->batch != p.batch || cache->hkv != p.hkv || cache->d != p.d || index->device != is_here.dev)
+        return LSA_ERR_INVALID_ARG;
     if (index->n_tokens + n_new > p.n_tokens + p.append_capacity) return LSA_ERR_INVALID_ARG;
     if (n_new == 0) return LSA_OK;
     return append_common(index, nullptr, cache, n_new, stream);
@@ -590,7 +600,8 @@ int lsa_append_cached(lsa_index* index, const lsa_kv_cache* cache, int64_t n_new
 int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, const void* Q, int64_t n,
                     const int64_t* cu, const int64_t* pos0, int32_t hq, int32_t dtype, const double* inv_freq,
                     int32_t rot, int32_t interleaved, void* K_out, void* Q_out, void* stream) {
-    if (!valid_cache(cache)) return LSA_ERR_INVALID_ARG;
+    const Here is_here;
+    if (!valid_cache(cache, is_here)) return LSA_ERR_INVALID_ARG;
     if (dtype != LSA_F32 && dtype != LSA_BF16) return LSA_ERR_INVALID_ARG;
     if (rot < 0 || rot > cache->d || rot % 16 || (rot > 0 && !is_here(inv_freq))) return LSA_ERR_INVALID_ARG;
     if (n < 0 || n > INT32_MAX || hq < 0 || hq > 4096 || !is_here(cu) || !is_here(pos0))
@@ -608,7 +619,8 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
 
 int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
                    int32_t hq, int32_t dtype, int32_t max_sel, void* O, float* lse, void* stream) {
-    if (!valid_cache(cache)) return LSA_ERR_INVALID_ARG;
+    const Here is_here;
+    if (!valid_cache(cache, is_here)) return LSA_ERR_INVALID_ARG;
     if (dtype != LSA_F32 && dtype != LSA_BF16) return LSA_ERR_INVALID_ARG;
     if (nq < 0 || nq > INT32_MAX || hq < cache->hkv || hq % cache->hkv || hq / cache->hkv > 64 || max_sel < 1)
         return LSA_ERR_INVALID_ARG;
