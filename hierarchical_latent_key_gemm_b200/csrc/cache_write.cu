@@ -43,8 +43,8 @@ struct WriteArgs {
     int most_tokens;       // of a unit
     int lists;             // rows of a token: its K heads, its V heads, its query heads
     // blockIdx.y, few tokens a page: per_cta lists each; whole pages: kv_ctas CTAs
-    // with kv_per KV heads each, then others with q_per query heads each, q_side of
-    // them side by side
+    // with kv_per KV heads each, then others with the query heads of q_per tokens
+    // each, q_side heads side by side
     int per_cta, kv_ctas, kv_per, q_per, q_side;
     int32_t* err;
 };
@@ -337,26 +337,26 @@ __device__ __forceinline__ void store_row(const WriteArgs& a, const Unit& u, con
     }
 }
 
-// Sines and cosines of the unit's tokens, for all their heads: [token][4][rot / 16]
-// float4, cos 0-3, cos 4-7, sin 0-3, sin 4-7 of 8 pairs.
+// Sines and cosines of the unit's tokens [t0, t1), for all their heads: [token][4]
+// [rot / 16] float4, cos 0-3, cos 4-7, sin 0-3, sin 4-7 of 8 pairs.
 template <typename T>
-__device__ __forceinline__ void fill_turns(const WriteArgs& a, const Unit& u, float4* turns) {
+__device__ __forceinline__ void fill_turns(const WriteArgs& a, const Unit& u, int t0, int t1, float4* turns) {
     const int n8 = a.rot / 16;
-    for (int i = threadIdx.x; i < u.m * n8; i += blockDim.x) {
+    for (int i = t0 * n8 + threadIdx.x; i < t1 * n8; i += blockDim.x) {
         const int t = i / n8, p = i % n8;
         float cs[8], sn[8];
         // the pairs of pieces a and b (see pieces_of)
         if (sizeof(T) == 2) turn8(a.inv_freq, 8 * p, 8, 0, u.pos + t, cs, sn);
         else if (a.interleaved) turn8(a.inv_freq, 2 * p, 2, 2 * n8, u.pos + t, cs, sn);
         else turn8(a.inv_freq, 4 * p, 4, 4 * n8, u.pos + t, cs, sn);
-        float4* at = turns + t * 4 * n8 + p;
+        float4* at = turns + (t - t0) * 4 * n8 + p;
         at[0] = make_float4(cs[0], cs[1], cs[2], cs[3]);
         at[n8] = make_float4(cs[4], cs[5], cs[6], cs[7]);
         at[2 * n8] = make_float4(sn[0], sn[1], sn[2], sn[3]);
         at[3 * n8] = make_float4(sn[4], sn[5], sn[6], sn[7]);
     }
 }
-// Turn the pieces x, y of a row of token t.
+// Turn the pieces x, y of a row of the t-th of these tokens.
 __device__ __forceinline__ void turn_row(const WriteArgs& a, const float4* turns, const Pieces& pc, int t, float* x,
                                          float* y) {
     const int n8 = a.rot / 16;
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(kWriteThreads) void cache_write_few_kernel(const Wr
     const Pieces pc = pieces_of<D, T>(a, tid % TPR);
     const int l0 = blockIdx.y * a.per_cta, l1 = min(a.lists, l0 + a.per_cta);
     const int le = kScaled ? max(l0, min(l1, 2 * a.c.hkv)) : l0;    // lists with a scale
-    fill_turns<T>(a, u, turn_s);
+    fill_turns<T>(a, u, 0, u.m, turn_s);
     for (int i = tid; i < le - l0; i += kWriteThreads) top_s[i] = 0;
     __syncthreads();
     if (l0 < le) {
@@ -457,8 +457,8 @@ __global__ __launch_bounds__(kMaxPageThreads) void cache_write_page_kernel(const
     const int tid = threadIdx.x, row = tid / TPR;
     const Pieces pc = pieces_of<D, T>(a, tid % TPR);
     const int y = blockIdx.y;
-    fill_turns<T>(a, u, turn_s);
     if (y < a.kv_ctas) {
+        fill_turns<T>(a, u, 0, u.m, turn_s);
         const int h0 = y * a.kv_per, h1 = min(a.c.hkv, h0 + a.kv_per);
         for (int i = tid; i < 2 * (h1 - h0); i += blockDim.x) top_s[i] = 0;
         __syncthreads();
@@ -529,12 +529,13 @@ __global__ __launch_bounds__(kMaxPageThreads) void cache_write_page_kernel(const
         }
         return;
     }
+    // all query heads of a share of the tokens, LT of a token's side by side, so that a warp's loads and stores are runs
+    const int t0 = (y - a.kv_ctas) * a.q_per, t1 = min(u.m, t0 + a.q_per);
+    fill_turns<T>(a, u, t0, t1, turn_s);
     __syncthreads();
-    // query heads: LT of a token's side by side, so that a warp's loads and stores are runs
-    const int h0 = (y - a.kv_ctas) * a.q_per, h1 = min(a.hq, h0 + a.q_per);
     const int LT = a.q_side, TT = ROWS / LT;
-    const int hh = h0 + row % LT;
-    for (int t = row / LT; t < u.m; t += TT) {
+    const int hh = row % LT, h1 = a.hq;
+    for (int t = t0 + row / LT; t < t1; t += TT) {
         const int64_t at = ((u.r0 + t) * a.hq + hh) * D;
         const T* src = static_cast<const T*>(a.Q) + at;
         T* out = static_cast<T*>(a.Q_out) + at;
@@ -553,7 +554,7 @@ __global__ __launch_bounds__(kMaxPageThreads) void cache_write_page_kernel(const
                     float p[8], q[8];
                     x[i].unpack(p);
                     w[i].unpack(q);
-                    if (pc.turned) turn_row(a, turn_s, pc, t, p, q);
+                    if (pc.turned) turn_row(a, turn_s, pc, t - t0, p, q);
                     store8(out + i * LT * D + pc.a, p, pc.gap);
                     store8(out + i * LT * D + pc.b, q, pc.gap);
                 }
@@ -589,17 +590,17 @@ int launch(WriteArgs a, int64_t units, bool pages, cudaStream_t s) {
                            turns + 2 * (size_t)a.per_cta * sizeof(float), s);
     }
     const int threads = std::min(kMaxPageThreads, std::max(64, a.c.page * (D / 16) / 2));
-    // few units: their heads are split over CTAs; a KV head is about three query heads' work
-    const int64_t want = 148 / 2 * kMaxPageThreads / threads;
+    // few units: their KV heads and their queries' tokens are split over CTAs; a KV head is about three query heads' work
+    const int64_t want = (int64_t)148 * kMaxPageThreads / threads;
     const int64_t most = std::max<int64_t>(1, (want + units / 2) / units), work = 3 * a.c.hkv + a.hq;
     const int64_t kv_ctas = std::min<int64_t>(a.c.hkv, std::max<int64_t>(1, (3 * a.c.hkv * most + work / 2) / work));
-    const int64_t q_ctas = std::min<int64_t>(a.hq, std::max<int64_t>(1, (a.hq * most + work / 2) / work));
+    const int64_t q_ctas = a.hq > 0 ? std::min<int64_t>(8, std::max<int64_t>(1, (a.hq * most + work / 2) / work)) : 0;
     a.kv_per = (int)((a.c.hkv + kv_ctas - 1) / kv_ctas);
-    a.q_per = a.hq > 0 ? (int)((a.hq + q_ctas - 1) / q_ctas) : 1;
     a.kv_ctas = (a.c.hkv + a.kv_per - 1) / a.kv_per;
+    a.q_per = (int)(q_ctas > 0 ? (a.c.page + q_ctas - 1) / q_ctas : 1);
     a.q_side = 1;
-    while (a.q_side * 2 <= std::min(a.q_per / rows_ahead<T>(), threads / (D / 16))) a.q_side *= 2;
-    const dim3 grid((unsigned)units, (unsigned)(a.kv_ctas + (a.hq + a.q_per - 1) / a.q_per));
+    while (a.q_side * 2 <= std::min(a.hq / rows_ahead<T>(), threads / (D / 16))) a.q_side *= 2;
+    const dim3 grid((unsigned)units, (unsigned)(a.kv_ctas + q_ctas));
     return launch_with(cache_write_page_kernel<D, T, CT>, a, grid, threads, turns + 2 * (size_t)a.kv_per * sizeof(float),
                        s);
 }
