@@ -18,7 +18,7 @@
 // shared memory by cp.async while it works on the step before, and looks the
 // rows of later steps up (token, page, scales) one load a step.  With that,
 // decode is bound by HBM (96 sequences, 32 heads of 128 over 4 KV heads, 2,624
-// rows of 8 bits: 47-51 us, 5.2-5.6 TB/s) and long chunks by instructions: the
+// rows of 8 bits: 46-51 us, 5.2-5.7 TB/s) and long chunks by instructions: the
 // conversion of the codes, two a cvt, on half the lanes of the ALU (2,048
 // queries x 16 heads, 3,136 rows: 311 us, 10.6 TB/s of rows, 169 TFLOP/s).
 //

@@ -406,7 +406,8 @@ int lsa_refresh_centroids(lsa_index* index, void* stream);
  * in bf16 or in 8 bits with a scale for each page and head.  The selection
  * (lsa_select) is unchanged; lsa_cache_write fills the pages, lsa_cache_attn
  * attends selection rows from them, lsa_append_cached keeps the index up from
- * them. */
+ * them.  All three take memory of the current device (or managed) only and
+ * refuse the rest as LSA_ERR_INVALID_ARG. */
 typedef struct {
     int64_t n_pages;           /* pages in the pools */
     int64_t batch;             /* sequences (rows of page_table) */
@@ -464,12 +465,13 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
 /* lsa_sparse_attn with the rows read from the cache: the same softmax over the
  * selected tokens of each row, keys and values being the cache's values.
  *  Q: device [batch][nq][hq][d] of dtype (LSA_F32 or LSA_BF16); idx, cnt as
- *      lsa_select writes them (entries past cnt are ignored); hq / hkv <= 64.
+ *      lsa_select writes them (entries past cnt are ignored); hq / hkv <= 64,
+ *      max_sel <= 2^30.
  *  O: device [batch][nq][hq][d] of dtype; lse: device float [batch][nq][hq] or
  *      NULL.  Q, O 16-byte aligned.
  * A row with cnt = 0 yields O = 0 and lse = -inf.  A token past the page table
  * or on a page id outside [0, n_pages) is skipped and latched as
- * LSA_ERR_DEVICE.  Only the selected tokens are read, so what stale or empty
+ * LSA_ERR_DEVICE; so is a cnt outside [0, max_sel], which is clamped.  Only the selected tokens are read, so what stale or empty
  * slots hold does not matter.  Sums, maxima and products are accumulated in
  * fp32; the same inputs give the same bits.  No allocation, one kernel:
  * capturable (after a first call on the device outside a capture). */

@@ -765,3 +765,42 @@ def test_a_long_row_over_a_cluster():
         Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
         assert lsa.lsa_check() == lsa.LSA_OK
         _check_attn(c, Q, idx, cnt, Oo, lse)
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Rotated keys without queries, on a stream given to the calls, with the current stream left alone."""
+    K, V, Q, cu = _new_tokens([33, 7], 2, 8, 64, BF, 130)
+    pos = torch.zeros(2, dtype=torch.int64, device="cuda")
+    f = _inv_freq(64)
+    c, ref = (_shuffled_cache(2, 64, 2, 64, 16, E4, 131) for _ in range(2))
+    _, want = lsa.lsa_cache_write(ref, K, V, cu, pos, inv_freq=f, want_K=True)
+    idx, cnt = _selection(np.random.RandomState(132), 2, 1, 2, 7, 7, [7, 3])
+    q = Q[:2].reshape(2, 1, 8, 64).contiguous()
+    wO, wl = lsa.lsa_cache_attn(ref, q, idx, cnt)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):               # outputs of the side stream's own
+        got, O, lse = torch.empty_like(K), torch.empty_like(q), torch.empty_like(wl)
+    none, k = lsa.lsa_cache_write(c, K, V, cu, pos, inv_freq=f, K_out=got, stream=side)
+    lsa.lsa_cache_attn(c, q, idx, cnt, O=O, lse=lse, stream=side)
+    torch.cuda.synchronize()
+    assert none is None and k is got and torch.equal(got, want)
+    assert torch.equal(O, wO) and torch.equal(lse, wl)
+    assert torch.equal(c.K.view(torch.uint8), ref.K.view(torch.uint8)) and torch.equal(c.K_scale, ref.K_scale)
+    assert lsa.lsa_check() == lsa.LSA_OK
+
+
+@pytest.mark.parametrize("dtype", [E4, BF])
+def test_write_again_from_an_earlier_position(dtype):
+    """Tokens taken back and written once more leave the pages as they were; shorter ones leave what is behind them."""
+    K, V, _, cu = _new_tokens([90], 2, 2, 64, BF, 140)
+    f = _inv_freq(64)
+    c = _shuffled_cache(1, 96, 2, 64, 32, dtype, 141)
+    at = lambda t: torch.tensor([t], device="cuda")
+    lsa.lsa_cache_write(c, K, V, cu, at(0), inv_freq=f)
+    before = [t.clone().view(torch.uint8) for t in (c.K, c.V)]
+    for t, m in ((41, 49), (41, 5), (32, 58), (0, 90), (89, 1)):
+        lsa.lsa_cache_write(c, K[t:t + m].contiguous(), V[t:t + m].contiguous(), at(0).repeat(2) + at(0).new_tensor([0, m]),
+                            at(t), inv_freq=f)
+        assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, (c.K, c.V))), (t, m)
+    assert lsa.lsa_check() == lsa.LSA_OK
