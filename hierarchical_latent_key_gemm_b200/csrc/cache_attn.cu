@@ -184,7 +184,10 @@ constexpr int min_ctas() {
 }
 
 // Tiles of 16 tokens of a warp's step.  Two steps are in shared memory: 8 KB of
-// rows each (4 KB of 64-byte rows).
+// rows each (4 KB of 64-byte rows).  For 128-byte rows one tile a step and the 16
+// warps an SM that then fit were slower: the long chunk above 365 us with two
+// steps in shared memory and 375 with three, against 311 (two tiles side by side
+// hide each other's latencies); 96 sequences 48.7 and 47.5 against 49.6.
 template <int D, typename CT>
 constexpr int tiles_per_step() { return D * sizeof(CT) <= 128 ? 2 : 1; }
 
@@ -210,6 +213,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     constexpr int STEP = 16 * TPS;                    // tokens of a warp's step
     constexpr int BUFFER = TPS * 2 * TILE;            // bytes of a step: (K tile, V tile) TPS times
     constexpr int LD = D + 4;                         // row stride of the merge buffers
+    static_assert(HG * LD * 4 <= 2 * BUFFER, "a warp's sums go where its rows were");
     extern __shared__ __align__(128) unsigned char ring_s[];   // [kWarps][2][BUFFER]; at the end [HG][LD] of a warp
     __shared__ float m_s[kWarps][HG], l_s[kWarps][HG];
     // what the CTAs of a cluster send: a share of the sums, and all maxima and sums of weights
