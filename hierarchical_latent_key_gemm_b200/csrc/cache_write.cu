@@ -50,7 +50,7 @@ struct WriteArgs {
     int by_token;          // units are tokens (few of them) instead of page slots
     int most_tokens;       // of a unit
     int lists;             // rows of a token: its K heads, its V heads, its query heads
-    // blockIdx.y, few tokens a page: per_cta lists each; whole pages: kv_ctas CTAs
+    // blockIdx.y, few tokens: per_cta lists each; many: kv_ctas CTAs
     // with kv_per KV heads each, then others with the query heads of q_per tokens
     // each, q_side heads side by side
     int per_cta, kv_ctas, kv_per, q_per, q_side;
@@ -192,21 +192,38 @@ struct Unit {
     int m, slot0, pid;
 };
 
-// The unit of this CTA (blockIdx.x); false where there is none.  Every CTA looks
-// all sequences over, so that a broken cu stops all of them.
+// The unit of this CTA (blockIdx.x); false where there is none.  Up to kScanned
+// sequences every CTA looks all of them over, so that a broken cu stops all CTAs;
+// of more it looks for its own in two steps, and all CTAs together look all over
+// (a token each for 1,024 sequences: 7.6 us with all looked over by every CTA, 6.6
+// in two steps; for 4,096: 43 and 35; for 65,535: 6.8 and 0.64 ms).
+constexpr int kScanned = 1024;
 __device__ __forceinline__ bool find_unit(const WriteArgs& a, Unit& u) {
-    __shared__ int found_b, broken;
+    __shared__ int found_b, broken, part;
     const CacheArgs& c = a.c;
     const int tid = threadIdx.x;
-    if (tid == 0) { found_b = -1; broken = 0; }
+    if (tid == 0) { found_b = -1; broken = 0; part = 0; }
     __syncthreads();
     const int64_t x = blockIdx.x;
-    for (int b = tid; b < a.batch; b += blockDim.x) {
+    // first unit of sequence b, whose first row is c0
+    auto unit0 = [&](int64_t c0, int64_t b) { return a.by_token ? c0 : (c0 >> c.log2_page) + 2 * b; };
+    auto look = [&](int b) {
         const int64_t c0 = a.cu[b], c1 = a.cu[b + 1];
         if (c0 < 0 || c1 < c0 || c1 > a.n) broken = 1;
-        const int64_t u0 = a.by_token ? c0 : (c0 >> c.log2_page) + 2 * (int64_t)b;
-        const int64_t u1 = a.by_token ? c1 : (c1 >> c.log2_page) + 2 * (int64_t)(b + 1);
-        if (x >= u0 && x < u1) found_b = b;
+        if (x >= unit0(c0, b) && x < unit0(c1, b + 1)) found_b = b;
+    };
+    if (a.batch <= kScanned) {
+#pragma unroll 4
+        for (int b = tid; b < a.batch; b += blockDim.x) look(b);
+    } else {
+        const int len = (a.batch + blockDim.x - 1) / blockDim.x;
+        if (tid * len < a.batch && x >= unit0(a.cu[tid * len], tid * len)) atomicMax(&part, tid);
+        const int share = (a.batch + gridDim.x - 1) / gridDim.x;
+        const int64_t s1 = min((int64_t)a.batch, (x + 1) * share);
+        for (int64_t b = x * share + tid; b < s1; b += blockDim.x) look((int)b);
+        __syncthreads();
+        const int b1 = min(a.batch, (part + 1) * len);
+        for (int b = part * len + tid; b < b1; b += blockDim.x) look(b);
     }
     __syncthreads();
     const int b = found_b;
@@ -379,13 +396,13 @@ __device__ __forceinline__ void turn_row(const WriteArgs& a, const float4* turns
     rotate16(x, y, cs, sn, a.interleaved);
 }
 
-// Few tokens a page: the unit's rows (token, list) in order, ROWS side by side.
+// Few tokens, or little: the unit's rows (token, list) in order, ROWS side by side.
 // The largest magnitudes of 8-bit pages take a pass of their own.
 template <int D, typename T, typename CT>
 __global__ __launch_bounds__(kWriteThreads) void cache_write_few_kernel(const WriteArgs a) {
     constexpr bool kScaled = sizeof(CT) == 1;
     constexpr int TPR = D / 16;                     // threads per row
-    constexpr int ROWS = kWriteThreads / TPR;
+    const int ROWS = blockDim.x / TPR;
     extern __shared__ float4 turn_s[];              // then [per_cta] largest magnitudes or inverse scales, [per_cta] shrinks
     uint32_t* top_s = reinterpret_cast<uint32_t*>(turn_s + a.most_tokens * (a.rot / 4));
     float *inv_s = reinterpret_cast<float*>(top_s), *shrink_s = inv_s + a.per_cta;
@@ -396,7 +413,7 @@ __global__ __launch_bounds__(kWriteThreads) void cache_write_few_kernel(const Wr
     const int l0 = blockIdx.y * a.per_cta, l1 = min(a.lists, l0 + a.per_cta);
     const int le = kScaled ? max(l0, min(l1, 2 * a.c.hkv)) : l0;    // lists with a scale
     fill_turns<T>(a, u, 0, u.m, turn_s);
-    for (int i = tid; i < le - l0; i += kWriteThreads) top_s[i] = 0;
+    for (int i = tid; i < le - l0; i += blockDim.x) top_s[i] = 0;
     __syncthreads();
     if (l0 < le) {
         const int lists = le - l0;
@@ -419,7 +436,7 @@ __global__ __launch_bounds__(kWriteThreads) void cache_write_few_kernel(const Wr
             if (pc.piece == 0) atomicMax(&top_s[l - l0], __float_as_uint(top));
         }
         __syncthreads();
-        for (int l = l0 + tid; l < le; l += kWriteThreads) {
+        for (int l = l0 + tid; l < le; l += blockDim.x) {
             const List<T> s = list_of<D, T>(a, u.r0, l);
             const float old = u.slot0 > 0 ? *scale_at(a, u, s) : 0.f;
             const float scale = fmaxf(new_scale(__uint_as_float(top_s[l - l0]), s.is_v), old);
@@ -447,7 +464,7 @@ __global__ __launch_bounds__(kWriteThreads) void cache_write_few_kernel(const Wr
     }
 }
 
-// Whole pages.  blockIdx.y: CTAs for KV heads, then CTAs for query heads.  A KV
+// Many tokens a page.  blockIdx.y: CTAs for KV heads, then CTAs for query heads.  A KV
 // head's K and V rows of the page are in registers while their scales are
 // settled, two tokens a thread, so they are read once; queries stream through,
 // several rows on their way in every thread.
@@ -596,7 +613,11 @@ int launch(WriteArgs a, int64_t units, bool pages, cudaStream_t s) {
         const int64_t most = std::min<int64_t>((a.lists * per_unit + ROWS - 1) / ROWS, (want + units - 1) / units);
         a.per_cta = (int)((a.lists + most - 1) / most);
         const dim3 grid((unsigned)units, (unsigned)((a.lists + a.per_cta - 1) / a.per_cta));
-        return launch_with(cache_write_few_kernel<D, T, CT>, a, grid, kWriteThreads,
+        // More CTAs than run at once (4 an SM): half the threads each, which have more to do (a token each
+        // for 4,096 sequences of 8 query and 1 KV heads 20.9 us against 35.2, 32 and 4 heads 31.2 and 46.7; of 96
+        // sequences, 32 and 4 heads, 5.3 and 5.0).
+        const int threads = (int64_t)grid.x * grid.y > 148 * 4 ? kWriteThreads / 2 : kWriteThreads;
+        return launch_with(cache_write_few_kernel<D, T, CT>, a, grid, threads,
                            turns + 2 * (size_t)a.per_cta * sizeof(float), s);
     }
     const int threads = std::min(kMaxPageThreads, std::max(64, a.c.page * (D / 16) / 2));
@@ -637,12 +658,17 @@ int launch_cache_write(const lsa_kv_cache& cache, const void* K, const void* V, 
     const int64_t units = a.by_token ? n : slots;
     a.most_tokens = (int)std::min<int64_t>(cache.page, n);
     a.lists = 2 * cache.hkv + hq;
-    // Whole pages are worth a kernel that reads them once when the sequences fill
-    // some, and when there is enough of it that reading twice leaves the caches
-    // (8-bit pages, 32 query and 4 KV heads of 128, few-token kernel and page kernel:
-    // 64 x 256 tokens in pages of 128 136 and 81 us, of 64 86.5 and 71.5, of 16 75.7
-    // and 67.8; 16 x 256 in pages of 16 18.7 and 25.6; 64 x 4 in pages of 64 6.1 and 8.9).
-    const bool pages = n >= cache.batch * cache.page && n * cache.page * cache.page >= (1 << 21);
+    // Tokens of a page are worth a kernel that reads them once when a sequence brings
+    // ten or more, and when there is enough of it: bytes of a unit's rows times bytes
+    // of all rows.  Few-token kernel and page kernel in microseconds, 32 query and 4 KV
+    // heads of 128, 8-bit pages, sequences x tokens: pages of 16, 16 x 16 (4.3e11) 6.3
+    // and 7.7, 16 x 32 (8.6e11) 8.6 and 7.2, 512 x 4 (8.6e11) 16.1 and 20.0; of 32, 300 x
+    // 10 (3.1e12) 29.8 and 19.8; of 64, 8 x 32 (8.6e11) 7.3 and 6.8, 64 x 256 127 and 71;
+    // of 128, 128 x 16 (3.4e12) 17.5 and 16.1, 512 x 8 (3.4e12) 39.8 and 56.5.  12 and 4 heads of
+    // 64, bf16 pages of 16: 64 x 64 (4.3e11) 8.0 and 11.1; of 64, 300 x 50 (4.9e12) 33.2 and 25.9.
+    const double token_bytes = (double)a.lists * cache.d * (dtype == LSA_F32 ? 4 : 2);
+    const double unit_bytes = token_bytes * std::min<int64_t>(cache.page, n / cache.batch);
+    const bool pages = n >= 10 * cache.batch && unit_bytes * (token_bytes * n) >= 5e11;
     if (cache.d == 128)
         return dtype == LSA_F32 ? launch_ct<128, float>(a, cache.dtype, units, pages, s)
                                 : launch_ct<128, __nv_bfloat16>(a, cache.dtype, units, pages, s);

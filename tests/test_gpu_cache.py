@@ -804,3 +804,65 @@ def test_write_again_from_an_earlier_position(dtype):
                             at(t), inv_freq=f)
         assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, (c.K, c.V))), (t, m)
     assert lsa.lsa_check() == lsa.LSA_OK
+
+
+@pytest.mark.parametrize("batch,most,page,dtype", [(3001, 3, 16, E4), (1025, 40, 16, E4), (2500, 2, 64, BF), (65535, 1, 16, E4)])
+def test_many_sequences(batch, most, page, dtype):
+    """More sequences than a CTA looks over: the pages of calls for a few hundred of them each."""
+    g = np.random.RandomState(batch)
+    lens = g.randint(0, most + 1, batch) if most < 40 else g.randint(10, most, batch)
+    n, pad = int(lens.sum()), 5
+    K, V, Q, cu = _new_tokens(list(lens), 1, 2, 64, BF, 150, pad=pad)
+    cu += 2                                     # padding on both sides
+    pos = torch.tensor(g.randint(0, 2 * page, batch), device="cuda")
+    f = _inv_freq(64)
+    c, ref = (lsa.make_kv_cache(batch, 5 * page, 1, 64, page, dtype=dtype) for _ in range(2))
+    q, k = torch.full_like(Q, 7), torch.full_like(K, 7)
+    lsa.lsa_cache_write(c, K, V, cu, pos, Q=Q, inv_freq=f, K_out=k, Q_out=q)
+    qr, kr = torch.full_like(Q, 7), torch.full_like(K, 7)
+    for b0 in range(0, batch, 1000):
+        b1 = min(batch, b0 + 1000)
+        part = lsa.KVCache(ref.K, ref.V, ref.page_table[b0:b1], ref.K_scale, ref.V_scale)
+        lsa.lsa_cache_write(part, K, V, cu[b0:b1 + 1], pos[b0:b1], Q=Q, inv_freq=f, K_out=kr, Q_out=qr)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    assert torch.equal(q, qr) and torch.equal(k, kr)
+    assert torch.all(q[:2] == 7) and torch.all(q[2 + n:] == 7)
+    for name in ("K", "V", "K_scale", "V_scale"):
+        a, b = getattr(c, name), getattr(ref, name)
+        if a is not None:
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+    bad = cu.clone()                            # a fall somewhere, and an end past the rows
+    bad[batch // 2] = n + 2 + pad
+    lsa.lsa_cache_write(c, K, V, bad, pos, Q=Q, inv_freq=f, K_out=k, Q_out=q)
+    assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+    bad = cu.clone()
+    bad[-1] = n + pad + 1
+    lsa.lsa_cache_write(c, K, V, bad, pos, Q=Q, inv_freq=f, K_out=k, Q_out=q)
+    assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE
+    assert lsa.lsa_check() == lsa.LSA_OK
+
+
+@pytest.mark.parametrize("lens,page,hkv,hq,d,io,dtype,rot,inter", [
+    ([300, 11, 700], 64, 8, 0, 128, BF, E4, 128, False),
+    ([10 + i % 11 for i in range(40)], 128, 4, 16, 128, F32, E4, 96, True),
+    ([900, 30, 500], 64, 3, 15, 64, BF, BF, 64, False),
+    ([19] * 60, 16, 2, 8, 128, F32, BF, 128, False),
+    ([12, 9] * 75, 32, 4, 8, 64, BF, E4, 32, True)])
+def test_write_by_pages_that_stay_part_empty(lens, page, hkv, hq, d, io, dtype, rot, inter):
+    """Enough rows for the kernel that reads them once, few of them in a page, from inside a page on; none of the
+    queries, or more of them than side by side."""
+    pos0 = [(7 * i + 3) % (2 * page) for i in range(len(lens))]
+    cache = _shuffled_cache(len(lens), max(lens) + 3 * page, hkv, d, page, dtype, 160)
+    if cache.scaled:
+        for name in "KV":
+            p = getattr(cache, name).view(torch.uint8)
+            p.copy_(torch.where((p & 0x7f) == 0x7f, p & 0x80, p))
+            getattr(cache, name + "_scale").fill_(2.0 ** -11)
+    before = _snapshot(cache)
+    K, V, Q, cu = _new_tokens(lens, hkv, hq, d, io, 161, pad=3)
+    pos = torch.tensor(pos0, dtype=torch.int64, device="cuda")
+    K_out, Q_out = torch.zeros_like(K), torch.zeros_like(Q) if hq else None
+    lsa.lsa_cache_write(cache, K, V, cu, pos, Q=Q, inv_freq=_inv_freq(rot), interleaved=inter, K_out=K_out, Q_out=Q_out)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    _check_write(cache, before, K, V, Q, K_out, Q_out, cu, pos, rot, inter)
+    assert torch.all(K_out[sum(lens):] == 0) and (Q is None or torch.all(Q_out[sum(lens):] == 0))
