@@ -18,9 +18,9 @@
 // shared memory by cp.async while it works on the step before, and looks the
 // rows of later steps up (token, page, scales) one load a step.  With that,
 // decode is bound by HBM (96 sequences, 32 heads of 128 over 4 KV heads, 2,624
-// rows of 8 bits: 46-51 us, 5.2-5.7 TB/s) and long chunks by instructions: the
+// rows of 8 bits: 47-52 us, 5.1-5.6 TB/s) and long chunks by instructions: the
 // conversion of the codes, two a cvt, on half the lanes of the ALU (2,048
-// queries x 16 heads, 3,136 rows: 311 us, 10.6 TB/s of rows, 169 TFLOP/s).
+// queries x 16 heads, 3,136 rows: 356 us, 9.2 TB/s of rows, 148 TFLOP/s).
 //
 // A warp takes 16 tokens at a time on the M side of mma.sync m16n8k16 (keys x
 // heads, then components x heads), so 8 heads fill a tile without padding; the
@@ -196,7 +196,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     constexpr bool E4 = sizeof(CT) == 1;              // 8-bit codes, fp16 products; else bf16
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int PQ = F32 ? (E4 ? 2 : 3) : 1;        // 16-bit parts of a query component
-    constexpr int PP = F32 ? (E4 ? 2 : 3) : (E4 ? 1 : 2);   // and of a weight
+    // And of a weight: two fp16 parts carry 22 bits (with one part, 11 bits, the long chunk above took 311 us against
+    // 356, and its O was 4.8e-4 of its norm from that of fp32 weights, now 7e-5; bf16 rounds it by 1.6e-3), two bf16
+    // parts 16, 2^-8 of what the rounding of bf16 results takes, three 24.
+    constexpr int PP = F32 && !E4 ? 3 : 2;
     // The tensor cores cut a running sum off at 24 bits without rounding.  For fp32
     // results sums are therefore kept outside, by rounded additions: every product of
     // a score, every step of acc (with sums in the tensor cores 7.7e-7 off the exact

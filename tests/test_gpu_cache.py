@@ -866,3 +866,22 @@ def test_write_by_pages_that_stay_part_empty(lens, page, hkv, hq, d, io, dtype, 
     assert lsa.lsa_check() == lsa.LSA_OK
     _check_write(cache, before, K, V, Q, K_out, Q_out, cu, pos, rot, inter)
     assert torch.all(K_out[sum(lens):] == 0) and (Q is None or torch.all(Q_out[sum(lens):] == 0))
+
+
+@pytest.mark.parametrize("nq,G,d", [(3, 8, 64), (2, 16, 128), (1, 5, 64), (2501, 4, 64)])
+def test_weights_carry_more_bits_than_the_output(nq, G, d):
+    """Two tokens whose values are 1 and -1: O is the difference of two weights that are nearly equal, so that its own
+    rounding is small and a weight's would show.  Scores are single products, exact but for the exponent's roundings:
+    2^-22 for each of two additions at up to 2^4, the exponential's 2^-22 and the weight's two halves of 11 bits
+    (2^-22) are off by less than 2^-20 of a weight together."""
+    c = lsa.make_kv_cache(1, 16, 1, d, page=16)
+    c.K[0, 0, 0, 0], c.K[0, 0, 1, 0] = 1.0, 1.125
+    c.V[0, 0, 0], c.V[0, 0, 1] = 1.0, -1.0
+    Q = torch.randn(1, nq, G, d, generator=_gen(170), device="cuda")
+    Q[..., 0] = torch.exp2(-5 + 3 * torch.rand(1, nq, G, generator=_gen(171), device="cuda"))
+    Q = Q.to(BF)
+    idx = torch.tensor([0, 1], dtype=torch.int32, device="cuda").expand(1, nq, 1, 2).contiguous()
+    Oo, _ = lsa.lsa_cache_attn(c, Q, idx, torch.full((1, nq, 1), 2, dtype=torch.int32, device="cuda"))
+    assert lsa.lsa_check() == lsa.LSA_OK
+    want = torch.tanh(-0.125 * Q[..., :1].double() / math.sqrt(d) / 2)
+    assert torch.all((Oo.double() - want).abs() <= HALF_STEP[BF] * want.abs() + 2.0 ** -20)
