@@ -20,7 +20,7 @@
 // decode is bound by HBM (96 sequences, 32 heads of 128 over 4 KV heads, 2,624
 // rows of 8 bits: 47-52 us, 5.1-5.6 TB/s) and long chunks by instructions: the
 // conversion of the codes, two a cvt, on half the lanes of the ALU (2,048
-// queries x 16 heads, 3,136 rows: 356 us, 9.2 TB/s of rows, 148 TFLOP/s).
+// queries x 16 heads, 3,136 rows: 368 us, 8.9 TB/s of rows, 143 TFLOP/s).
 //
 // A warp takes 16 tokens at a time on the M side of mma.sync m16n8k16 (keys x
 // heads, then components x heads), so 8 heads fill a tile without padding; the
@@ -191,20 +191,24 @@ constexpr int min_ctas() {
 template <int D, typename CT>
 constexpr int tiles_per_step() { return D * sizeof(CT) <= 128 ? 2 : 1; }
 
-template <int D, typename CT, typename T, int NT>
+// EXACT: acc is added up outside the tensor cores (always for fp32 results)
+template <int D, typename CT, typename T, int NT, bool EXACT>
 __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_attn_kernel(const AttnArgs a) {
     constexpr bool E4 = sizeof(CT) == 1;              // 8-bit codes, fp16 products; else bf16
     constexpr bool F32 = sizeof(T) == 4;
+    static_assert(EXACT || !F32, "fp32 results");
     constexpr int PQ = F32 ? (E4 ? 2 : 3) : 1;        // 16-bit parts of a query component
     // And of a weight: two fp16 parts carry 22 bits (with one part, 11 bits, the long chunk above took 311 us against
     // 356, and its O was 4.8e-4 of its norm from that of fp32 weights, now 7e-5; bf16 rounds it by 1.6e-3), two bf16
     // parts 16, 2^-8 of what the rounding of bf16 results takes, three 24.
     constexpr int PP = F32 && !E4 ? 3 : 2;
-    // The tensor cores cut a running sum off at 24 bits without rounding.  For fp32
-    // results sums are therefore kept outside, by rounded additions: every product of
-    // a score, every step of acc (with sums in the tensor cores 7.7e-7 off the exact
-    // result on the median, 4.9e-7 so; of rows of 2,000 to 3,000 up to 9e-6).
-    constexpr bool SUMS = F32;
+    // The tensor cores cut a running sum off at 24 bits without rounding.  Sums over
+    // d and, where EXACT, acc over the steps of a row are therefore kept outside, by
+    // rounded additions (fp32: with sums in the tensor cores 7.7e-7 off the exact result on
+    // the median, 4.9e-7 so; of rows of 2,000 to 3,000 up to 9e-6; bf16, the long chunk:
+    // scores outside halve the error of lse to 6.6e-8, 368 us against 356; acc, too, 394).
+    // Without EXACT acc is cut off four times a step (two of 16 tokens), each time by
+    // less than 2^-23 of it: by 2^-15 at most over the steps that launch allows.
     constexpr int KS = D / 16;                        // k steps of K Q^T, m tiles of V^T P^T
     constexpr int MV = E4 ? 2 : 1;                    // m tiles of a V load
     constexpr int HG = 8 * NT;                        // heads of a warp
@@ -445,7 +449,6 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     for (int nt = 0; nt < NT; ++nt) {
                         float* acc = (s & 1) ? z[nt] : y[half][nt];
                         if (s < 2 && p == 0) mma_first<E4>(acc, ka, qf[p][s][nt]);
-                        else if constexpr (!SUMS) mma<E4>(acc, ka, qf[p][s][nt]);
                         else {
                             float sum[4];
                             mma_first<E4>(sum, ka, qf[p][s][nt]);
@@ -550,7 +553,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
         // ---- acc: rows g and g + 8 of m tile i are components 16 i + g and 16 i + g + 8
 #pragma unroll
         for (int i = 0; i < KS; i += MV) {
-            float sum[MV][NT][4];      // of this step (fp32, see SUMS)
+            float sum[MV][NT][4];      // of this step (EXACT)
 #pragma unroll
             for (int half = 0; half < TPS; ++half) {
                 uint32_t va[MV][4];
@@ -575,12 +578,12 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     for (int q = 0; q < PP; ++q)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (!SUMS) mma<E4>(o[i + x][nt], va[x], pb[half][q][nt]);
+                            if constexpr (!EXACT) mma<E4>(o[i + x][nt], va[x], pb[half][q][nt]);
                             else if (half == 0 && q == 0) mma_first<E4>(sum[x][nt], va[x], pb[half][q][nt]);
                             else mma<E4>(sum[x][nt], va[x], pb[half][q][nt]);
                         }
             }
-            if constexpr (SUMS)
+            if constexpr (EXACT)
 #pragma unroll
                 for (int x = 0; x < MV; ++x)
 #pragma unroll
@@ -697,7 +700,7 @@ constexpr size_t ring_bytes() { return (size_t)kWarps * 2 * tiles_per_step<D, CT
 
 // How many clusters of `size` CTAs the current device runs at once (a property of
 // the kernel and the device, asked for once); 0 where it cannot.
-template <int D, typename CT, typename T, int NT>
+template <int D, typename CT, typename T, int NT, bool EXACT>
 int resident(int size) {
     static std::atomic<int> known[128][5];            // + 1
     int dev = 0, lg = 0;
@@ -705,7 +708,7 @@ int resident(int size) {
     while ((1 << lg) < size) ++lg;
     int n = known[dev][lg].load(std::memory_order_relaxed) - 1;
     if (n >= 0) return n;
-    const auto kernel = cache_attn_kernel<D, CT, T, NT>;
+    const auto kernel = cache_attn_kernel<D, CT, T, NT, EXACT>;
     n = 0;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes<D, CT>());
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -730,33 +733,11 @@ int resident(int size) {
     return n;
 }
 
-template <int D, typename CT, typename T, int NT>
-int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
-    a.groups = (a.G + 8 * NT - 1) / (8 * NT);
-    const int64_t units = rows * a.groups;
-    a.units = (uint32_t)units;
-    const int step = 16 * tiles_per_step<D, CT>();
-    const int64_t steps = (a.max_sel + step - 1) / step;
-    const int64_t ctas = resident<D, CT, T, NT>(1);
-    if (ctas < 1) return LSA_ERR_CUDA;
-    // Few rows: a cluster of CTAs shares each, while all of them run at once and
-    // every warp has a step (4 rows of 4,160 tokens, 16 heads of 128, 8-bit pages:
-    // 8.7 us with 16 CTAs a row, 10.4 with 8, 14.5 with 4, 35 with one; 128 rows of up
-    // to 1,599, 4 heads of 64, bf16: 10.7 with 2, 12.5 with one, 15.0 with 4).
-    a.cluster = 1;
-    while (a.cluster < kMaxCluster && a.cluster * 2 * kWarps <= steps &&
-           units <= resident<D, CT, T, NT>(a.cluster * 2))
-        a.cluster *= 2;
-    // Many rows: a warp takes a whole one, which needs no merge, unless the last
-    // round of warps would then run long.  In microseconds a CTA that shares a row
-    // takes about 4 + steps / 4, four whole rows side by side 6 + steps (8 heads of
-    // 128, 8-bit pages; 4,096 rows of 64 tokens: 39 us shared, 21 whole; 16,384 of
-    // 512: 299 and 227; 1,024 of 2,048: 59 and 66).
-    const int64_t shared = (units + ctas - 1) / ctas * (4 + (steps + kWarps - 1) / kWarps);
-    const int64_t whole = (units + kWarps * ctas - 1) / (kWarps * ctas) * (6 + steps);
-    a.warps = a.cluster == 1 && whole < shared ? 1 : kWarps;
+template <int D, typename CT, typename T, int NT, bool EXACT>
+int launch_split(const AttnArgs& a, cudaStream_t s) {
+    if (resident<D, CT, T, NT, EXACT>(a.cluster) < 1) return LSA_ERR_CUDA;      // sets the kernel's attributes, too
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.warps == 1 ? (units + kWarps - 1) / kWarps : units * a.cluster));
+    cfg.gridDim = dim3(a.warps == 1 ? (a.units + kWarps - 1) / kWarps : a.units * a.cluster);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.dynamicSmemBytes = ring_bytes<D, CT>();
@@ -767,7 +748,43 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     note_launch();
-    return cuda_status(cudaLaunchKernelEx(&cfg, cache_attn_kernel<D, CT, T, NT>, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, cache_attn_kernel<D, CT, T, NT, EXACT>, a));
+}
+
+// Steps of a warp up to which bf16 results are added up inside the tensor cores
+// (EXACT: 8 % longer for the long chunk above, whose warps take 25 steps).
+constexpr int64_t kCutSteps = 64;
+
+template <int D, typename CT, typename T, int NT>
+int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
+    constexpr bool F32 = sizeof(T) == 4;
+    a.groups = (a.G + 8 * NT - 1) / (8 * NT);
+    const int64_t units = rows * a.groups;
+    a.units = (uint32_t)units;
+    const int step = 16 * tiles_per_step<D, CT>();
+    const int64_t steps = (a.max_sel + step - 1) / step;
+    const int64_t ctas = resident<D, CT, T, NT, F32>(1);
+    if (ctas < 1) return LSA_ERR_CUDA;
+    // Few rows: a cluster of CTAs shares each, while all of them run at once and
+    // every warp has a step (4 rows of 4,160 tokens, 16 heads of 128, 8-bit pages:
+    // 8.7 us with 16 CTAs a row, 10.4 with 8, 14.5 with 4, 35 with one; 128 rows of up
+    // to 1,599, 4 heads of 64, bf16: 10.7 with 2, 12.5 with one, 15.0 with 4).
+    a.cluster = 1;
+    while (a.cluster < kMaxCluster && a.cluster * 2 * kWarps <= steps &&
+           units <= resident<D, CT, T, NT, F32>(a.cluster * 2))
+        a.cluster *= 2;
+    // Many rows: a warp takes a whole one, which needs no merge, unless the last
+    // round of warps would then run long.  In microseconds a CTA that shares a row
+    // takes about 4 + steps / 4, four whole rows side by side 6 + steps (8 heads of
+    // 128, 8-bit pages; 4,096 rows of 64 tokens: 39 us shared, 21 whole; 16,384 of
+    // 512: 299 and 227; 1,024 of 2,048: 59 and 66).
+    const int64_t shared = (units + ctas - 1) / ctas * (4 + (steps + kWarps - 1) / kWarps);
+    const int64_t whole = (units + kWarps * ctas - 1) / (kWarps * ctas) * (6 + steps);
+    a.warps = a.cluster == 1 && whole < shared ? 1 : kWarps;
+    if constexpr (!F32)
+        if (steps <= kCutSteps * (a.warps == 1 ? 1 : kWarps * a.cluster))
+            return launch_split<D, CT, T, NT, false>(a, s);
+    return launch_split<D, CT, T, NT, true>(a, s);
 }
 
 template <int D, typename CT>

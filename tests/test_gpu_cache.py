@@ -885,3 +885,30 @@ def test_weights_carry_more_bits_than_the_output(nq, G, d):
     assert lsa.lsa_check() == lsa.LSA_OK
     want = torch.tanh(-0.125 * Q[..., :1].double() / math.sqrt(d) / 2)
     assert torch.all((Oo.double() - want).abs() <= HALF_STEP[BF] * want.abs() + 2.0 ** -20)
+
+
+def test_acc_of_long_rows_is_rounded_not_cut_off():
+    """Values 1 in a row's first half, -1 in its second, under weights that are no short numbers: acc climbs to half of
+    the weights' sum and back, and what every addition cuts off is left over (2.3e-5 where the tensor cores add).
+    Scores are single products.  Bounds: a weight 2^-20 as in the test above; acc over the S = 1,563 steps of a warp,
+    rounded to nearest once a step, by 2^-24 of half the sum at most, each way alike: six standard deviations of S such
+    roundings; the products of a step cut off four times by 2^-23 of them."""
+    n, nq, d = 200_000, 300, 64
+    c = lsa.make_kv_cache(1, n, 1, d, page=128)
+    g = _gen(172)
+    c.K[:, 0, :, 0] = (1 + torch.randint(0, 8, (c.K.shape[0], 128), generator=g, device="cuda") / 8.0).to(E4)
+    t = torch.arange(c.K.shape[0] * 128, device="cuda").view(-1, 128)
+    c.V[:, 0] = torch.where(t < n // 2, 1.0, -1.0)[..., None].to(E4)
+    Q = torch.zeros(1, nq, 2, d, device="cuda")
+    Q[..., 0] = 0.5 + torch.rand(1, nq, 2, generator=g, device="cuda")
+    Q = Q.to(BF)
+    idx = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, nq, 1, n).contiguous()
+    cnt = torch.full((1, nq, 1), n, dtype=torch.int32, device="cuda")
+    Oo, _ = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    w = torch.exp(Q[0, :, :, :1].double() * c.K[:, 0, :, 0].double().flatten()[:n] / math.sqrt(d))
+    v = c.V[:, 0, :, 0].double().flatten()[:n]
+    want = (w @ v / w.sum(-1))[None, ..., None]
+    S = -(-n // (4 * 32))
+    tol = 2.0 ** -20 + 6 * math.sqrt(S / 3) * 2.0 ** -25 + 2.0 ** -21
+    assert torch.all((Oo.double() - want).abs() <= HALF_STEP[BF] * want.abs() + tol)
