@@ -615,7 +615,8 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
             if (g == 0) {
-                m_s[warp][head] = unset[nt][e] ? -INFINITY : m[nt][e];
+                // a head whose every score is NaN stays unset: its l is NaN and reaches the output, unlike that of no token
+                m_s[warp][head] = unset[nt][e] && s == 0.f ? -INFINITY : m[nt][e];
                 l_s[warp][head] = s;
             }
 #pragma unroll

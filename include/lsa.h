@@ -470,10 +470,11 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
  *      max_sel <= 2^30.
  *  O: device [batch][nq][hq][d] of dtype; lse: device float [batch][nq][hq] or
  *      NULL.  Q, O 16-byte aligned.
- * A row with cnt = 0 yields O = 0 and lse = -inf.  A token past the page table
- * or on a page id outside [0, n_pages) is skipped and latched as
- * LSA_ERR_DEVICE; so is a cnt outside [0, max_sel], which is clamped.  Only the selected tokens are read, so what stale or empty
- * slots hold does not matter.  Sums, maxima and products are accumulated in
+ * A row with cnt = 0 yields O = 0 and lse = -inf; a head with a score that is NaN
+ * yields NaN in both.  A token past the page table or on a page id outside [0,
+ * n_pages) is skipped and latched as LSA_ERR_DEVICE; so is a cnt outside [0,
+ * max_sel], which is clamped.  Only the selected tokens are read, so what stale
+ * or empty slots hold does not matter.  Sums, maxima and products are accumulated in
  * fp32; the same inputs give the same bits.  No allocation, one kernel:
  * capturable (after a first call on the device outside a capture). */
 int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,

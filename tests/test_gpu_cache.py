@@ -912,3 +912,39 @@ def test_acc_of_long_rows_is_rounded_not_cut_off():
     S = -(-n // (4 * 32))
     tol = 2.0 ** -20 + 6 * math.sqrt(S / 3) * 2.0 ** -25 + 2.0 ** -21
     assert torch.all((Oo.double() - want).abs() <= HALF_STEP[BF] * want.abs() + tol)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("nq", [1, 2, 2501])
+def test_scores_that_are_all_nan_give_nan(io, nq):
+    """A head whose every score is NaN (a NaN among its queries, or among the only key of its row) is no empty row, in
+    a row of its own warp, of a CTA or of a cluster."""
+    c = _filled(1, 2048, 1, 128, 64, E4, 180)
+    Q = torch.randn(1, nq, 4, 128, generator=_gen(181), device="cuda").to(io)
+    n = 2048 if nq < 100 else 40
+    idx = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, nq, 1, n).contiguous()
+    cnt = torch.full((1, nq, 1), n, dtype=torch.int32, device="cuda")
+    Q[0, nq - 1, 2, 77] = math.nan
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert torch.isnan(Oo[0, nq - 1, 2]).all() and torch.isnan(lse[0, nq - 1, 2])
+    assert torch.isnan(Oo).sum() == 128 and torch.isnan(lse).sum() == 1
+    Q[0, nq - 1, 2, 77] = 0
+    # one token, its key NaN
+    c.K.view(torch.uint8)[int(c.page_table[0, 0]), 0, 5, 9] = 0x7f
+    idx[0, nq - 1, 0, 0], cnt[0, nq - 1] = 5, 1
+    if nq > 1:
+        cnt[0, :nq - 1] = 5                     # without token 5
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert torch.isnan(Oo[0, nq - 1]).all() and torch.isnan(lse[0, nq - 1]).all()
+    assert torch.isfinite(Oo[0, :nq - 1].float()).all() and torch.isfinite(lse[0, :nq - 1]).all()
+    # the empty row stays what it is
+    cnt[0, nq - 1] = 0
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert torch.all(Oo[0, nq - 1] == 0) and torch.all(lse[0, nq - 1] == -math.inf)
+    # a run of tokens that one CTA of a cluster takes
+    c.K.view(torch.uint8)[c.page_table[0, :2].long()] = 0x7f
+    idx[0, :, 0] = torch.arange(n, dtype=torch.int32, device="cuda")
+    cnt.fill_(n)
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert torch.isnan(Oo).all() and torch.isnan(lse).all()
+    assert lsa.lsa_check() == lsa.LSA_OK
