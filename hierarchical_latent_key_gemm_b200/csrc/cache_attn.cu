@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
         }
     }
     if (n < 0 || n > a.max_sel) {
-        if (tid == 0) latch(a.err, kErrDevice);
+        if (lane == 0) latch(a.err, kErrDevice);      // every warp: it may have a row of its own
         n = n < 0 ? 0 : a.max_sel;
     }
     const int steps = (n + STEP - 1) / STEP;

@@ -948,3 +948,23 @@ def test_scores_that_are_all_nan_give_nan(io, nq):
     Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
     assert torch.isnan(Oo).all() and torch.isnan(lse).all()
     assert lsa.lsa_check() == lsa.LSA_OK
+
+
+def test_a_bad_count_is_latched_whichever_warp_has_its_row():
+    nq, n = 2501, 50
+    c = _filled(1, 400, 1, 64, 32, E4, 190)
+    Q = torch.randn(1, nq, 4, 64, generator=_gen(191), device="cuda").to(BF)
+    idx, cnt = _selection(np.random.RandomState(192), 1, nq, 1, n, 400, [n, 0, 17])
+    want = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    for row in (0, 1, 2, 3, 1230, nq - 1):
+        for bad in (-1, n + 1, -2 ** 31, 2 ** 31 - 1):
+            k, x = cnt.clone(), idx.clone()
+            k[0, row], x[0, row] = bad, idx[0, 0]
+            Oo, lse = lsa.lsa_cache_attn(c, Q, x, k)
+            assert lsa.lsa_check() == lsa.LSA_ERR_DEVICE, (row, bad)
+            keep = torch.arange(nq, device="cuda") != row
+            assert torch.equal(Oo[0, keep], want[0][0, keep]) and torch.equal(lse[0, keep], want[1][0, keep])
+            if bad < 0:                         # clamped
+                assert torch.all(Oo[0, row] == 0) and torch.all(lse[0, row] == -math.inf)
+    assert lsa.lsa_check() == lsa.LSA_OK
