@@ -26,6 +26,7 @@
 // another): 4.5 us for 4 sequences, 4.7 for 96.  8,191 fp32 tokens of 8 query and 2
 // KV heads into pages of 128 are one wave of 130 CTAs: 19 us.
 #include <algorithm>
+#include <atomic>
 
 #include "cache_common.cuh"
 
@@ -589,14 +590,23 @@ __global__ __launch_bounds__(kMaxPageThreads) void cache_write_page_kernel(const
     }
 }
 
-template <typename K>
-int launch_with(K kernel, const WriteArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t s) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// What a launch may ask for: the sines of a page's tokens and two words a list of a token.
+constexpr int kMaxShared = 128 * (128 / 4) * (int)sizeof(float4) + 2 * (2 * 1024 + 4096) * (int)sizeof(float);
+
+// The limit of a kernel's shared memory is set once a device, to the same for all
+// calls: two threads that set what their calls need would lower each other's.
+template <auto Kernel>
+int launch_with(const WriteArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+    static std::atomic<bool> set[128];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return LSA_ERR_CUDA;
+    if (!set[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
         if (e != cudaSuccess) return cuda_status(e);
+        set[dev].store(true, std::memory_order_relaxed);
     }
     note_launch();
-    kernel<<<grid, threads, smem, s>>>(a);
+    Kernel<<<grid, threads, smem, s>>>(a);
     return cuda_status(cudaGetLastError());
 }
 
@@ -617,8 +627,8 @@ int launch(WriteArgs a, int64_t units, bool pages, cudaStream_t s) {
         // for 4,096 sequences of 8 query and 1 KV heads 20.9 us against 35.2, 32 and 4 heads 31.2 and 46.7; of 96
         // sequences, 32 and 4 heads, 5.3 and 5.0).
         const int threads = (int64_t)grid.x * grid.y > 148 * 4 ? kWriteThreads / 2 : kWriteThreads;
-        return launch_with(cache_write_few_kernel<D, T, CT>, a, grid, threads,
-                           turns + 2 * (size_t)a.per_cta * sizeof(float), s);
+        return launch_with<cache_write_few_kernel<D, T, CT>>(a, grid, threads,
+                                                             turns + 2 * (size_t)a.per_cta * sizeof(float), s);
     }
     const int threads = std::min(kMaxPageThreads, std::max(64, a.c.page * (D / 16) / 2));
     // few units: their KV heads and their queries' tokens are split over CTAs; a KV head is about three query
@@ -633,8 +643,8 @@ int launch(WriteArgs a, int64_t units, bool pages, cudaStream_t s) {
     a.q_side = 1;
     while (a.q_side * 2 <= std::min(a.hq / rows_ahead<T>(), threads / (D / 16))) a.q_side *= 2;
     const dim3 grid((unsigned)units, (unsigned)(a.kv_ctas + q_ctas));
-    return launch_with(cache_write_page_kernel<D, T, CT>, a, grid, threads, turns + 2 * (size_t)a.kv_per * sizeof(float),
-                       s);
+    return launch_with<cache_write_page_kernel<D, T, CT>>(a, grid, threads, turns + 2 * (size_t)a.kv_per * sizeof(float),
+                                                          s);
 }
 
 template <int D, typename T>

@@ -968,3 +968,49 @@ def test_a_bad_count_is_latched_whichever_warp_has_its_row():
             if bad < 0:                         # clamped
                 assert torch.all(Oo[0, row] == 0) and torch.all(lse[0, row] == -math.inf)
     assert lsa.lsa_check() == lsa.LSA_OK
+
+
+def test_write_whose_shared_memory_just_fits_the_default():
+    """127 tokens x 96 turned components and 48 lists a CTA: 49,152 bytes next to what the kernel holds by itself."""
+    hkv, hq, d, page, B = 32, 128, 128, 128, 127
+    K, V, Q, cu = _new_tokens([1] * B, hkv, hq, d, BF, 200)
+    pos = torch.arange(B, device="cuda")
+    c, ref = (lsa.make_kv_cache(B, page, hkv, d, page) for _ in range(2))
+    q, k = lsa.lsa_cache_write(c, K, V, cu, pos, Q=Q, inv_freq=_inv_freq(96), want_K=True)
+    for b in range(0, B, 40):
+        e = min(B, b + 40)
+        part = lsa.KVCache(ref.K, ref.V, ref.page_table[b:e], ref.K_scale, ref.V_scale)
+        qr, kr = lsa.lsa_cache_write(part, K[b:e], V[b:e], cu[:e - b + 1], pos[b:e], Q=Q[b:e], inv_freq=_inv_freq(96),
+                                     want_K=True)
+        assert torch.equal(q[b:e], qr) and torch.equal(k[b:e], kr)
+    for name in ("K", "V", "K_scale", "V_scale"):
+        assert torch.equal(getattr(c, name).view(torch.uint8), getattr(ref, name).view(torch.uint8))
+    assert lsa.lsa_check() == lsa.LSA_OK
+
+
+def test_writes_from_two_host_threads():
+    """Calls of different sizes from two threads at once: what one asks of the driver does not reach the other's."""
+    import threading
+    sets = []
+    for k, (rot, tokens) in enumerate(((128, 128), (112, 128))):
+        lens = [1] * tokens
+        K, V, Q, cu = _new_tokens(lens, 2, 4, 128, BF, 210 + k)
+        sets.append((lsa.make_kv_cache(tokens, 128, 2, 128, 128), K, V, cu, torch.zeros(tokens, dtype=torch.int64,
+                     device="cuda"), Q, _inv_freq(rot), torch.empty_like(Q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(c, K, V, cu, pos, Q, f, Q_out, stream):
+        try:
+            for _ in range(2000):
+                lsa.lsa_cache_write(c, K, V, cu, pos, Q=Q, inv_freq=f, Q_out=Q_out, stream=stream)
+        except Exception as e:      # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=s) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and lsa.lsa_check() == lsa.LSA_OK
