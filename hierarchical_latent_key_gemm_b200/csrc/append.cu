@@ -209,11 +209,16 @@ __global__ __launch_bounds__(kAppThreads) void append_insert_kernel(const AppArg
     }
 }
 
+// Shared memory that any call may take (d, r up to 128; kMaxNear bytes of new latents):
+// the kernels' limits are always set to it, so that the calls of two threads do
+// not lower each other's.
+constexpr int kMaxLatent = (128 * 128 + 128) * (int)sizeof(float), kMaxNear = 200 * 1024;
+
 template <typename Keys>
 int launch_latent(const Keys& keys, const AppArgs& a, int64_t units, cudaStream_t s) {
     const size_t smem = (size_t)(a.d * a.r + a.d) * sizeof(float);
     const cudaError_t e = cudaFuncSetAttribute(append_latent_kernel<Keys>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+                                               kMaxLatent);
     if (e != cudaSuccess) return cuda_status(e);
     note_launch();
     append_latent_kernel<Keys><<<dim3((unsigned)a.n_new, (unsigned)units), kAppThreads, smem, s>>>(keys, a);
@@ -257,7 +262,7 @@ int launch_append(lsa_index* ix, const void* K, const lsa_kv_cache* cache, int64
     a.n_new = n_new_blocks;
     a.err = ix->err;
     const size_t smem_near = (size_t)n_new_blocks * p.r * sizeof(float);
-    if (smem_near > 200 * 1024) return LSA_ERR_INVALID_ARG;
+    if (smem_near > (size_t)kMaxNear) return LSA_ERR_INVALID_ARG;
     Arena scratch;
     scratch.async = true;
     scratch.stream = s;
@@ -272,7 +277,7 @@ int launch_append(lsa_index* ix, const void* K, const lsa_kv_cache* cache, int64
         st = p.dtype == LSA_F32 ? launch_latent(DenseKeys<float>{(const float*)K}, a, ix->units, s)
                                 : launch_latent(DenseKeys<__nv_bfloat16>{(const __nv_bfloat16*)K}, a, ix->units, s);
     if (st != LSA_OK) return st;
-    cudaError_t e = cudaFuncSetAttribute(append_nearest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_near);
+    cudaError_t e = cudaFuncSetAttribute(append_nearest_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxNear);
     if (e != cudaSuccess) return cuda_status(e);
     dim3 gnear((unsigned)((ix->L + kLeavesPerCta - 1) / kLeavesPerCta), (unsigned)ix->units);
     note_launch();

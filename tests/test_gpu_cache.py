@@ -1014,3 +1014,34 @@ def test_writes_from_two_host_threads():
         t.join()
     torch.cuda.synchronize()
     assert not failed and lsa.lsa_check() == lsa.LSA_OK
+
+
+def test_appends_from_two_host_threads():
+    """Indexes of different widths kept up from two caches by two threads at once."""
+    import threading
+    n0, steps, jobs, failed = 256, 600, [], []
+    for k, (d, r, pool, per) in enumerate(((128, 128, 1, 1), (128, 16, 1, 1), (64, 64, 1, 200))):
+        cache = _filled(1, n0 + steps, 1, d, 32, BF, 260 + k)
+        dense = torch.randn(1, n0 + steps, 1, d, generator=_gen(261), device="cuda").to(BF)
+        W = torch.linalg.qr(torch.randn(d, d, generator=_gen(262), device="cuda"))[0][:, :r].contiguous()
+        bp = lsa.make_build_params(1, n0, n0 + steps, 1, d, r, pool, lsa.LSA_BF16, (8,), 2, 0, 0, steps)
+        jobs.append((lsa.lsa_build_index(bp, dense, W), cache, per, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(ix, cache, per, stream):
+        try:
+            for _ in range(steps // per):
+                lsa.lsa_append_cached(ix, cache, per, stream=stream)
+        except Exception as e:      # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for ix, *_ in jobs:
+        assert lsa.lsa_check(ix) in (lsa.LSA_OK, lsa.LSA_ERR_CAPACITY)     # 8 leaves may fill up
+        ix.free()
+    assert not failed
