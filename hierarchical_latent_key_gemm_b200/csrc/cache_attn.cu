@@ -18,9 +18,9 @@
 // shared memory by cp.async while it works on the step before, and looks the
 // rows of later steps up (token, page, scales) one load a step.  With that,
 // decode is bound by HBM (96 sequences, 32 heads of 128 over 4 KV heads, 2,624
-// rows of 8 bits: 47-52 us, 5.1-5.6 TB/s) and long chunks by instructions: the
+// rows of 8 bits: 47-53 us, 5.0-5.6 TB/s) and long chunks by instructions: the
 // conversion of the codes, two a cvt, on half the lanes of the ALU (2,048
-// queries x 16 heads, 3,136 rows: 368 us, 8.9 TB/s of rows, 143 TFLOP/s).
+// queries x 16 heads, 3,136 rows: 377 us, 8.7 TB/s of rows, 139 TFLOP/s).
 //
 // A warp takes 16 tokens at a time on the M side of mma.sync m16n8k16 (keys x
 // heads, then components x heads), so 8 heads fill a tile without padding; the
@@ -38,6 +38,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cache_common.cuh"
 #include "warp_mma.cuh"
@@ -51,10 +52,17 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 16;
 // Weights are at most 2^(kHeadroom + kLazy) and the largest at least 2^kHeadroom:
-// the maximum is renewed only when a score passes it by 2^kLazy.  In fp16 a
-// weight keeps 11 bits down to 2^-(14 + kHeadroom) of the largest, and what lies
-// below 2^-(25 + kHeadroom) of it is lost.
-constexpr float kLazy = 8.f, kHeadroom = 6.f;
+// the maximum is renewed only when a score passes it by 2^kLazy.  Two fp16 parts
+// keep 22 bits of a weight down to 2^-3 and nothing below 2^-25, 2^-32 of the largest.
+constexpr float kLazy = 8.f, kHeadroom = 7.f;
+// The weights hold the V scale, and a component of O may come from pages of small
+// scales alone.  Steps with a scale 2^kScales below the largest so far take their
+// weights by size, those within a factor of 2^kClass at a time, which keeps 22 bits of
+// all that fp32 can hold; so a weight loses no more than 2^-(32 - kScales) of the largest
+// softmax weight.  The look at the scales and the factors in two parts took the long
+// chunk from 368 to 377 us, 4 sequences from 9.2 to 9.9.
+constexpr int kScales = 4;
+constexpr float kClass = 14.f;
 
 struct AttnArgs {
     CacheArgs c;
@@ -381,6 +389,7 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     float o[KS][NT][4];
     // m: reference of a head's exponents, its largest so far less kHeadroom; unset: no score yet above -inf
     float m[NT][2], l[NT][2];
+    int most = 0;                                     // largest V scale so far, its exponent field
     bool unset[NT][2], any_unset = true;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -514,9 +523,10 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     unset[nt][e] = first && up == -INFINITY;
                     any_unset |= unset[nt][e];
                     if (first ? up == -INFINITY : !(up > 0.f)) up = 0.f;
-                    const float f = first ? 1.f : ex2(-up);
+                    // the root of the factor, for two products: it may be below what fp32 can hold when l and o are not
+                    const float f = first ? 1.f : ex2(-0.5f * up);
                     m[nt][e] += up;
-                    l[nt][e] *= f;
+                    l[nt][e] = l[nt][e] * f * f;
 #pragma unroll
                     for (int half = 0; half < TPS; ++half) {
                         y[half][nt][e] -= up;
@@ -524,72 +534,123 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
                     }
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
-                        o[i][nt][e] *= f;
-                        o[i][nt][e + 2] *= f;
+                        o[i][nt][e] = o[i][nt][e] * f * f;
+                        o[i][nt][e + 2] = o[i][nt][e + 2] * f * f;
                     }
                 }
         }
         // ---- weights: B fragments of P^T
         uint32_t pb[TPS][PP][NT][2];
+        auto put_weights = [&](int half, int nt, const float* w) {
+            uint32_t lo[PP], hi[PP];
+            split<E4, PP>(w[0], w[1], lo);
+            split<E4, PP>(w[2], w[3], hi);
 #pragma unroll
-        for (int half = 0; half < TPS; ++half)
+            for (int p = 0; p < PP; ++p) {
+                pb[half][p][nt][0] = movmatrix_t(lo[p]);
+                pb[half][p][nt][1] = movmatrix_t(hi[p]);
+            }
+        };
+        // ---- acc: rows g and g + 8 of m tile i are components 16 i + g and 16 i + g + 8; OUTSIDE: the step's products
+        // are summed first and added `times` over
+        auto add_products = [&](auto outside, float times) {
+            constexpr bool OUTSIDE = decltype(outside)::value;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
+            for (int i = 0; i < KS; i += MV) {
+                float sum[MV][NT][4];
+#pragma unroll
+                for (int half = 0; half < TPS; ++half) {
+                    uint32_t va[MV][4];
+                    // 32 bytes of every row: of 256-byte rows the second 128 are a fixed distance on
+                    constexpr int NV = (int)(sizeof(vp) / 4);
+                    const int j = i / MV;
+                    const uint32_t p = vp[j % NV] + (half * 2 * TILE + 128 * (j / NV));
+                    if constexpr (E4) {
+                        uint32_t w[4];
+                        load_transposed(p, w);
+#pragma unroll
+                        for (int x = 0; x < MV; ++x) {
+                            e4m3x4_to_f16x4(w[2 * x], va[x][0], va[x][2]);
+                            e4m3x4_to_f16x4(w[2 * x + 1], va[x][1], va[x][3]);
+                        }
+                    } else {
+                        ldsm_x4_t(p, va[0][0], va[0][1], va[0][2], va[0][3]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < MV; ++x)
+#pragma unroll
+                        for (int q = 0; q < PP; ++q)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if constexpr (!OUTSIDE) mma<E4>(o[i + x][nt], va[x], pb[half][q][nt]);
+                                else if (half == 0 && q == 0) mma_first<E4>(sum[x][nt], va[x], pb[half][q][nt]);
+                                else mma<E4>(sum[x][nt], va[x], pb[half][q][nt]);
+                            }
+                }
+                if constexpr (OUTSIDE)
+#pragma unroll
+                    for (int x = 0; x < MV; ++x)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[i + x][nt][e] = fmaf(sum[x][nt][e], times, o[i + x][nt][e]);
+            }
+        };
+        bool apart = false;
+        if constexpr (E4) {
+            const int field = cur.ok >> lane & 1u ? __float_as_int(cur.vs) >> 23 : most;
+            if (__any_sync(0xffffffffu, (uint32_t)(most - field) > (uint32_t)kScales)) {
+                most = max(most, __reduce_max_sync(0xffffffffu, field));
+                apart = __any_sync(0xffffffffu, (cur.ok >> lane & 1u) && field < most - kScales);
+            }
+        }
+        if (!apart) {
+#pragma unroll
+            for (int half = 0; half < TPS; ++half)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = ex2(y[half][nt][e]);
+                        l[nt][e & 1] = fmaf(w[e], iv[half][e >> 1], l[nt][e & 1]);
+                    }
+                    put_weights(half, nt, w);
+                }
+            add_products(std::integral_constant<bool, EXACT>{}, 1.f);
+        } else {
+            float low = INFINITY;      // smallest exponent whose weight fp32 can hold
+#pragma unroll
+            for (int half = 0; half < TPS; ++half)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    w[e] = ex2(y[half][nt][e]);
-                    l[nt][e & 1] = fmaf(w[e], iv[half][e >> 1], l[nt][e & 1]);
-                }
-                uint32_t lo[PP], hi[PP];
-                split<E4, PP>(w[0], w[1], lo);
-                split<E4, PP>(w[2], w[3], hi);
+                    const float lv = __shfl_sync(0xffffffffu, lg, 16 * half + krow + KROW * (e >> 1));
 #pragma unroll
-                for (int p = 0; p < PP; ++p) {
-                    pb[half][p][nt][0] = movmatrix_t(lo[p]);
-                    pb[half][p][nt][1] = movmatrix_t(hi[p]);
-                }
-            }
-        // ---- acc: rows g and g + 8 of m tile i are components 16 i + g and 16 i + g + 8
-#pragma unroll
-        for (int i = 0; i < KS; i += MV) {
-            float sum[MV][NT][4];      // of this step (EXACT)
-#pragma unroll
-            for (int half = 0; half < TPS; ++half) {
-                uint32_t va[MV][4];
-                // 32 bytes of every row: of 256-byte rows the second 128 are a fixed distance on
-                constexpr int NV = (int)(sizeof(vp) / 4);
-                const int j = i / MV;
-                const uint32_t p = vp[j % NV] + (half * 2 * TILE + 128 * (j / NV));
-                if constexpr (E4) {
-                    uint32_t w[4];
-                    load_transposed(p, w);
-#pragma unroll
-                    for (int x = 0; x < MV; ++x) {
-                        e4m3x4_to_f16x4(w[2 * x], va[x][0], va[x][2]);
-                        e4m3x4_to_f16x4(w[2 * x + 1], va[x][1], va[x][3]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float v = y[half][nt][e];
+                        l[nt][e & 1] += ex2(v - lv);
+                        if (v > -125.f) low = fminf(low, v);
                     }
-                } else {
-                    ldsm_x4_t(p, va[0][0], va[0][1], va[0][2], va[0][3]);
                 }
+            // from `up` down to `up - kClass`, times 2^down; NaN with the first
+            float up = kHeadroom + kLazy, down = 0.f;
+            for (bool more = true; more; up -= kClass, down += kClass) {
 #pragma unroll
-                for (int x = 0; x < MV; ++x)
+                for (int half = 0; half < TPS; ++half)
 #pragma unroll
-                    for (int q = 0; q < PP; ++q)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w[4];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (!EXACT) mma<E4>(o[i + x][nt], va[x], pb[half][q][nt]);
-                            else if (half == 0 && q == 0) mma_first<E4>(sum[x][nt], va[x], pb[half][q][nt]);
-                            else mma<E4>(sum[x][nt], va[x], pb[half][q][nt]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float v = y[half][nt][e];
+                            const bool mine = down == 0.f ? !(v <= up - kClass) : v <= up && v > up - kClass;
+                            w[e] = mine ? ex2(v + down) : 0.f;
                         }
+                        put_weights(half, nt, w);
+                    }
+                add_products(std::true_type{}, ex2(-down));
+                more = __any_sync(0xffffffffu, low <= up - kClass);
             }
-            if constexpr (EXACT)
-#pragma unroll
-                for (int x = 0; x < MV; ++x)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i + x][nt][e] += sum[x][nt][e];
         }
         __syncwarp();          // the buffer is free
         cur = next;
@@ -637,8 +698,8 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
     for (int w = 0; w < kWarps; ++w) {
         f[w] = 0.f;
         if (w >= w0 && w < w1 && M != -INFINITY) {
-            f[w] = ex2(m_s[w][head] - M);
-            L += f[w] * l_s[w][head];
+            f[w] = ex2(0.5f * (m_s[w][head] - M));    // the root, as above
+            L += f[w] * l_s[w][head] * f[w];
         }
     }
     const float* part = reinterpret_cast<const float*>(ring_s) + head * LD;
@@ -649,8 +710,8 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
         for (int w = 0; w < kWarps; ++w)
             if (w >= w0 && w < w1) {
                 const float2 v = *reinterpret_cast<const float2*>(part + w * (2 * BUFFER / 4) + 2 * q);
-                s.x += f[w] * v.x;
-                s.y += f[w] * v.y;
+                s.x += f[w] * v.x * f[w];
+                s.y += f[w] * v.y * f[w];
             }
         return s;
     };
@@ -685,11 +746,11 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
         for (int r = 0; r < a.cluster; ++r) top = fmaxf(top, m_r[r][hd]);
         float2 s = make_float2(0.f, 0.f);
         for (int r = 0; r < a.cluster; ++r) {
-            const float fr = top == -INFINITY ? 0.f : ex2(m_r[r][hd] - top);
+            const float fr = top == -INFINITY ? 0.f : ex2(0.5f * (m_r[r][hd] - top));
             const float2 v = sum_r[r * share + j];
-            sum += fr * l_r[r][hd];
-            s.x += fr * v.x;
-            s.y += fr * v.y;
+            sum += fr * l_r[r][hd] * fr;
+            s.x += fr * v.x * fr;
+            s.y += fr * v.y * fr;
         }
         put2(out + hd * D + 2 * q, sum == 0.f ? 0.f : s.x / sum, sum == 0.f ? 0.f : s.y / sum);
         if (a.lse && q == 0) a.lse[q0 / D + hd] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;

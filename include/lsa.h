@@ -474,9 +474,13 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
  * yields NaN in both.  A token past the page table or on a page id outside [0,
  * n_pages) is skipped and latched as LSA_ERR_DEVICE; so is a cnt outside [0,
  * max_sel], which is clamped.  Only the selected tokens are read, so what stale
- * or empty slots hold does not matter.  Sums, maxima and products are accumulated in
- * fp32; the same inputs give the same bits.  No allocation, one kernel:
- * capturable (after a first call on the device outside a capture). */
+ * or empty slots hold does not matter.  Sums and maxima are fp32.  In the
+ * products bf16 queries are exact, fp32 ones have 22 bits next to LSA_E4M3 pages
+ * and 24 next to LSA_BF16; softmax weights have 22 bits next to LSA_E4M3 pages
+ * (to 2^-28 of a head's largest), whatever the scales of the pages, and next to
+ * LSA_BF16 24 for fp32 results and 16 for bf16 ones.  The same inputs give the same
+ * bits.  No allocation, one kernel: capturable (after a first call on the device
+ * outside a capture). */
 int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
                    int32_t hq, int32_t dtype, int32_t max_sel, void* O, float* lse, void* stream);
 

@@ -1045,3 +1045,52 @@ def test_appends_from_two_host_threads():
         assert lsa.lsa_check(ix) in (lsa.LSA_OK, lsa.LSA_ERR_CAPACITY)     # 8 leaves may fill up
         ix.free()
     assert not failed
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("d,G", [(64, 4), (128, 16)])
+@pytest.mark.parametrize("low,high", [(-4, 1), (-10, 0), (-12, 12), (-20, 20), (-50, 50), (-64, 64)])
+def test_values_on_pages_of_far_smaller_scales(io, d, G, low, high):
+    """Components that only pages of small scales fill, next to pages of large ones whose codes are zero there: each
+    component of O is a sum of its own, to the accuracy of the others."""
+    page, pages, n = 16, 40, 640
+    c = _filled(1, n, 1, d, page, E4, 220)
+    lo = torch.rand(pages, generator=_gen(221), device="cuda") < 0.5
+    lo[0], lo[1] = True, False
+    pid = c.page_table[0].long()
+    V = torch.randn(pages, page, d, generator=_gen(222), device="cuda").clamp(-3, 3) * 100
+    V[~lo, :, :d // 2] = 0
+    V[2] = 0                                    # a page of zeros
+    c.V.view(torch.uint8)[pid] = V.to(E4).view(torch.uint8)[:, None]
+    c.V_scale[pid, 0] = torch.exp2(torch.where(lo, float(low), float(high)))
+    c.V_scale[pid[2], 0] = 2.0 ** -64
+    Q = torch.randn(1, 8, G, d, generator=_gen(223), device="cuda").to(io)
+    g = np.random.RandomState(224)
+    idx, cnt = _selection(g, 1, 8, 1, n, n, [n, 300, 33, 2, 100, 64, 17, 500])
+    for i in range(1, 8, 2):                    # in any order
+        m = int(cnt[0, i])
+        idx[0, i, 0, :m] = idx[0, i, 0, torch.tensor(g.permutation(m), device="cuda")]
+    idx[0, 3, 0, :2] = torch.tensor([16, 3])    # one token of each
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    k, v = _values(c, "K"), _values(c, "V")
+    table, q = c.page_table[0].cpu().numpy(), Q.double().cpu().numpy()
+    for i in range(8):
+        t = idx[0, i, 0, :int(cnt[0, i])].cpu().numpy()
+        kk, vv = k[table[t // page], 0, t % page], v[table[t // page], 0, t % page]
+        s = q[0, i] @ kk.T / math.sqrt(d)
+        p = np.exp(s - s.max(1, keepdims=True))
+        z = np.log(p.sum(1)) + s.max(1)
+        p /= p.sum(1, keepdims=True)
+        # scores as in _check_attn; weights in 22 bits, or to 2^-28 of the largest; sums of n terms; a weight times its
+        # scale is nothing below 2^-125, where the largest is 2^7 at least
+        ds = 2.0 ** -24 * (d + 8) * (np.abs(q[0, i]) @ np.abs(kk).T).max(1, keepdims=True) / math.sqrt(d) + 2.0 ** -20
+        some = (np.abs(vv) * p.max(1)[:, None, None]).sum(1)
+        tol = (p @ np.abs(vv)) * (2 * ds + 2.0 ** -23 * len(t)) + 2.0 ** -28 * some
+        sc = c.V_scale[:, 0].double().cpu().numpy()[table[t // page]]
+        tol = tol + 2.0 ** -132 * (p * sc).max(1, keepdims=True) * (np.abs(vv) / sc[:, None]).sum(0)
+        want = p @ vv
+        tol = tol + HALF_STEP[io] * np.abs(want)
+        err = np.abs(Oo[0, i].double().cpu().numpy() - want)
+        assert np.all(err <= tol), (i, len(t), float((err / np.maximum(tol, 1e-300)).max()))
+        assert np.all(np.abs(lse[0, i].cpu().numpy() - z) <= ds[:, 0] + 2.0 ** -23 * (len(t) + np.abs(z)))
