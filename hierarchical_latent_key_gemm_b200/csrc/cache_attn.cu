@@ -491,7 +491,8 @@ __global__ __launch_bounds__(kThreads, (min_ctas<D, CT, T, NT>())) void cache_at
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float& v = y[half][nt][2 * e + i];
-                        v = fmaf(v, ks * qs[nt][i], lv - m[nt][i]);
+                        // ks first: v * ks stays in range, ks * qs may not
+                        v = fmaf(v * ks, qs[nt][i], lv - m[nt][i]);
                         top = fmaxf(top, v);
                     }
             }

@@ -1094,3 +1094,22 @@ def test_values_on_pages_of_far_smaller_scales(io, d, G, low, high):
         err = np.abs(Oo[0, i].double().cpu().numpy() - want)
         assert np.all(err <= tol), (i, len(t), float((err / np.maximum(tol, 1e-300)).max()))
         assert np.all(np.abs(lse[0, i].cpu().numpy() - z) <= ds[:, 0] + 2.0 ** -23 * (len(t) + np.abs(z)))
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_large_queries_on_keys_of_large_pages_that_are_zero(io):
+    """Queries of 2^90 on a page with the largest scale: where the products are zero the scores are, too."""
+    c = lsa.make_kv_cache(1, 32, 1, 64, page=16)
+    c.K[:, :, 3, 0] = 1.0
+    c.K[1, 0, :, 1] = 2.0
+    c.K_scale[0], c.K_scale[1] = 2.0 ** 64, 2.0 ** -64
+    c.V.copy_(torch.randn(c.V.shape, generator=_gen(230), device="cuda").to(E4))
+    Q = torch.zeros(1, 1, 2, 64, device="cuda")
+    Q[..., 1] = 2.0 ** 66                       # scores of 0 on page 0, of 2^66 2^-64 2 / 8 = 1 on page 1
+    Q[0, 0, 1, 5] = 2.0 ** 90                   # no key has this component
+    Q = Q.to(io)
+    idx = torch.tensor([[[[1, 3, 17, 19, 30]]]], dtype=torch.int32, device="cuda")
+    cnt = torch.full((1, 1, 1), 5, dtype=torch.int32, device="cuda")
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    _check_attn(c, Q[:, :, :1].contiguous(), idx, cnt, Oo[:, :, :1], lse[:, :, :1])
+    assert torch.isfinite(Oo.float()).all() and torch.isfinite(lse).all()
