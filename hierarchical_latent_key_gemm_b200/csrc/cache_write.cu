@@ -234,6 +234,7 @@ __device__ __forceinline__ bool find_unit(const WriteArgs& a, Unit& u) {
     }
     if (b < 0) return false;
     const int64_t c0 = a.cu[b], c1 = a.cu[b + 1], p0 = a.pos0[b];
+    if (c0 == c1) return false;        // has page slots, but no token whose position would matter
     if (p0 < 0) {
         if (tid == 0) latch(a.err, kErrDevice);
         return false;

@@ -431,8 +431,8 @@ typedef struct {
  *  cu: device int64 [batch+1], ascending: rows cu[b] .. cu[b+1]-1 are the new
  *      tokens of sequence b, at positions pos0[b], pos0[b]+1, ... (device int64
  *      [batch]); pos0[b] tokens are in its pages already.  A sequence may bring
- *      no token; rows outside [cu[0], cu[batch]) (padding) are not read and
- *      their outputs not written.
+ *      no token (its pos0 may be anything); rows outside [cu[0], cu[batch])
+ *      (padding) are not read and their outputs not written.
  *  inv_freq: device double [rot/2] or NULL with rot = 0.  Pair i of a token at
  *      position t is turned by t * inv_freq[i]: (x, y) -> (x cos - y sin,
  *      x sin + y cos).  rot: a multiple of 16, 0 <= rot <= d; pair i is

@@ -1113,3 +1113,16 @@ def test_large_queries_on_keys_of_large_pages_that_are_zero(io):
     Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
     _check_attn(c, Q[:, :, :1].contiguous(), idx, cnt, Oo[:, :, :1], lse[:, :, :1])
     assert torch.isfinite(Oo.float()).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("tokens", [2, 200])
+def test_a_sequence_without_a_token_has_no_position(tokens):
+    """Idle sequences marked by a position of -1, whether units are tokens or page slots."""
+    K, V, _, cu = _new_tokens([tokens], 2, 2, 64, BF, 240)
+    c, ref = (lsa.make_kv_cache(3, 256, 2, 64, page=16) for _ in range(2))
+    cu = torch.tensor([0, 0, tokens, tokens], dtype=torch.int64, device="cuda")
+    for pos, to in (([-1, 5, -1], c), ([0, 5, 0], ref)):
+        lsa.lsa_cache_write(to, K, V, cu, torch.tensor(pos, device="cuda"), inv_freq=_inv_freq(64))
+        assert lsa.lsa_check() == lsa.LSA_OK
+    for name in ("K", "V", "K_scale", "V_scale"):
+        assert torch.equal(getattr(c, name).view(torch.uint8), getattr(ref, name).view(torch.uint8))
