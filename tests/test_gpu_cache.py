@@ -1126,3 +1126,28 @@ def test_a_sequence_without_a_token_has_no_position(tokens):
         assert lsa.lsa_check() == lsa.LSA_OK
     for name in ("K", "V", "K_scale", "V_scale"):
         assert torch.equal(getattr(c, name).view(torch.uint8), getattr(ref, name).view(torch.uint8))
+
+
+@pytest.mark.parametrize("io,dtype,d", [(BF, E4, 128), (F32, E4, 64), (BF, BF, 64), (F32, BF, 128)])
+@pytest.mark.parametrize("rows", [1, 60, 1000])
+def test_every_step_of_a_long_row_reaches_the_output(io, dtype, d, rows):
+    """Token j's value is 1 in component (j // 16) % d only, and every score is 0: a component counts the tokens of its
+    tiles, of which there are 50 at most, and a tile of 16 tokens left out, taken twice or taken for another is 2 % of
+    some component, whose bound is 0.4 %."""
+    n = {1: 16 * d * 49, 60: 16 * d * 3, 1000: 8 * d}[rows] + 5
+    c = lsa.make_kv_cache(1, n, 1, d, 64, dtype=dtype)
+    t = torch.arange(n, device="cuda")
+    raw = torch.zeros(n, d, device="cuda")
+    raw[t, t // 16 % d] = 1.0
+    pages = torch.zeros(c.V.shape[0] * 64, d, device="cuda")
+    pages[:n] = raw
+    c.V.copy_(pages.view(-1, 1, 64, d).to(dtype))
+    Q = torch.randn(1, rows, 3, d, generator=_gen(250), device="cuda").to(io)
+    idx = t.int().expand(1, rows, 1, n).contiguous()
+    cnt = torch.full((1, rows, 1), n, dtype=torch.int32, device="cuda")
+    Oo, lse = lsa.lsa_cache_attn(c, Q, idx, cnt)
+    assert lsa.lsa_check() == lsa.LSA_OK
+    want = raw.double().sum(0) / n
+    # equal weights and small whole numbers: exact sums, one quotient and its rounding
+    assert torch.all((Oo.double() - want).abs() <= (HALF_STEP[io] + 2.0 ** -22) * want)
+    assert torch.all((lse.double() - math.log(n)).abs() <= 2.0 ** -20)
