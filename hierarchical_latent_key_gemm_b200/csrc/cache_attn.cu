@@ -40,6 +40,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "ask_once.cuh"
 #include "cache_common.cuh"
 #include "warp_mma.cuh"
 
@@ -765,35 +766,33 @@ constexpr size_t ring_bytes() { return (size_t)kWarps * 2 * tiles_per_step<D, CT
 // the kernel and the device, asked for once); 0 where it cannot.
 template <int D, typename CT, typename T, int NT, bool EXACT>
 int resident(int size) {
-    static std::atomic<int> known[128][5];            // + 1
+    static std::atomic<int> known[128][5];
     int dev = 0, lg = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
     while ((1 << lg) < size) ++lg;
-    int n = known[dev][lg].load(std::memory_order_relaxed) - 1;
-    if (n >= 0) return n;
-    const auto kernel = cache_attn_kernel<D, CT, T, NT, EXACT>;
-    n = 0;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes<D, CT>());
-    if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(size);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = ring_bytes<D, CT>();
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = size;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    }
-    if (e != cudaSuccess) {
+    return ask_once(known[dev][lg], [size] {
+        const auto kernel = cache_attn_kernel<D, CT, T, NT, EXACT>;
+        int n = 0;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring_bytes<D, CT>());
+        if (e == cudaSuccess && size > 8)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(size);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = ring_bytes<D, CT>();
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = size;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        }
+        if (e == cudaSuccess) return n;
         cudaGetLastError();
-        n = 0;
-    }
-    known[dev][lg].store(n + 1, std::memory_order_relaxed);
-    return n;
+        return e == cudaErrorInvalidClusterSize ? 0 : -1;
+    });
 }
 
 template <int D, typename CT, typename T, int NT, bool EXACT>

@@ -188,3 +188,21 @@ def test_c_calls_refuse_null_and_bad_caches():
         assert L.lsa_cache_attn(C.byref(bad), one, one, one, 1, 4, lsa.LSA_BF16, 9, one, None, None) == inv
         assert L.lsa_cache_write(C.byref(bad), one, one, None, 1, one, one, 0, lsa.LSA_BF16, None, 0, 0, None, None,
                                  None) == inv
+
+
+def test_a_failed_question_to_the_driver_is_asked_again():
+    """csrc/ask_once.cuh: answers are kept, zero among them; a failure is not."""
+    src = ('#include "ask_once.cuh"\n#include <cstdio>\nint main() {\n'
+           '    std::atomic<int> known{0};\n    int asked = 0, answers[] = {-1, -1, 0, 7};\n'
+           '    auto ask = [&] { return answers[asked++]; };\n'
+           '    for (int i = 0; i < 5; ++i) printf("%d ", lsa::ask_once(known, ask));\n'
+           '    printf("%d ", asked);\n    known = 0;\n'
+           '    for (int i = 0; i < 2; ++i) printf("%d ", lsa::ask_once(known, ask));\n'
+           '    printf("%d\\n", asked);\n    return 0;\n}\n')
+    with tempfile.TemporaryDirectory() as td:
+        c, exe = os.path.join(td, "t.cpp"), os.path.join(td, "t")
+        open(c, "w").write(src)
+        subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "hierarchical_latent_key_gemm_b200", "csrc"), c,
+                        "-o", exe], check=True)
+        out = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()
+    assert out == ["0"] * 5 + ["3"] + ["7", "7"] + ["4"]
