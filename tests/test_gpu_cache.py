@@ -1151,3 +1151,52 @@ def test_every_step_of_a_long_row_reaches_the_output(io, dtype, d, rows):
     # equal weights and small whole numbers: exact sums, one quotient and its rounding
     assert torch.all((Oo.double() - want).abs() <= (HALF_STEP[io] + 2.0 ** -22) * want)
     assert torch.all((lse.double() - math.log(n)).abs() <= 2.0 ** -20)
+
+
+def test_forms_first_used_inside_a_capture():
+    """In a process of its own: one call of the library outside a capture, then writes and attentions of other types and
+    sizes, used for the first time while they are captured."""
+    import os
+    import subprocess
+    import sys
+    src = """
+import torch
+from hierarchical_latent_key_gemm_b200 import lsa
+assert lsa.lsa_check() == lsa.LSA_OK
+def forms():
+    for dtype, io, d, n in ((torch.float8_e4m3fn, torch.bfloat16, 128, 1), (torch.float8_e4m3fn, torch.bfloat16, 128, 700),
+                            (torch.bfloat16, torch.float32, 64, 130), (torch.float8_e4m3fn, torch.float32, 128, 70)):
+        c = lsa.make_kv_cache(2, 1024, 2, d, 128, dtype=dtype)
+        g = torch.Generator(device="cuda").manual_seed(d + n)
+        K, V, Q = (torch.randn(2 * n, h, d, generator=g, device="cuda").to(io) for h in (2, 2, 8))
+        f = 10000.0 ** (-torch.arange(d // 2, dtype=torch.float64, device="cuda") / (d // 2))
+        cu = torch.tensor([0, n, 2 * n], device="cuda")
+        idx = torch.arange(n, dtype=torch.int32, device="cuda").expand(2, 1, 2, n).contiguous()
+        s = dict(c=c, K=K, V=V, Q=Q, f=f, cu=cu, pos=cu[:2] * 0, idx=idx, cnt=torch.full((2, 1, 2), n, dtype=torch.int32,
+                 device="cuda"), q=torch.zeros_like(Q), k=torch.zeros_like(K),
+                 O=torch.zeros(2, 1, 8, d, dtype=io, device="cuda"), lse=torch.zeros(2, 1, 8, device="cuda"))
+        yield s
+def call(s):
+    lsa.lsa_cache_write(s["c"], s["K"], s["V"], s["cu"], s["pos"], Q=s["Q"], inv_freq=s["f"], Q_out=s["q"], K_out=s["k"])
+    lsa.lsa_cache_attn(s["c"], s["q"][:2].view(2, 1, 8, -1), s["idx"], s["cnt"], O=s["O"], lse=s["lse"])
+a, b = list(forms()), list(forms())
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for s in a:
+        call(s)
+graph.replay()
+for s in b:
+    call(s)
+torch.cuda.synchronize()
+for x, y in zip(a, b):
+    for name in ("q", "k", "O", "lse"):
+        assert torch.equal(x[name], y[name]), name
+    assert torch.equal(x["c"].K.view(torch.uint8), y["c"].K.view(torch.uint8))
+assert lsa.lsa_check() == lsa.LSA_OK
+del graph
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", src], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
