@@ -622,8 +622,9 @@ int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx,
     const Here is_here;
     if (!valid_cache(cache, is_here)) return LSA_ERR_INVALID_ARG;
     if (dtype != LSA_F32 && dtype != LSA_BF16) return LSA_ERR_INVALID_ARG;
-    if (nq < 0 || nq > INT32_MAX || hq < cache->hkv || hq % cache->hkv || hq / cache->hkv > 64 || max_sel < 1 || max_sel > (1 << 30))
+    if (nq < 0 || nq > INT32_MAX || hq < cache->hkv || hq % cache->hkv || hq / cache->hkv > 64)
         return LSA_ERR_INVALID_ARG;
+    if (max_sel < 1 || max_sel > (1 << 30)) return LSA_ERR_INVALID_ARG;
     if (nq == 0) return LSA_OK;
     if (cache->batch * nq * hq > INT32_MAX) return LSA_ERR_INVALID_ARG;
     if (!is_here(Q) || !is_here(idx) || !is_here(cnt) || !is_here(O) || !aligned16(Q) ||

@@ -18,9 +18,9 @@
 // shared memory by cp.async while it works on the step before, and looks the
 // rows of later steps up (token, page, scales) one load a step.  With that,
 // decode is bound by HBM (96 sequences, 32 heads of 128 over 4 KV heads, 2,624
-// rows of 8 bits: 47-53 us, 5.0-5.6 TB/s) and long chunks by instructions: the
+// rows of 8 bits: 47-54 us, 4.9-5.6 TB/s) and long chunks by instructions: the
 // conversion of the codes, two a cvt, on half the lanes of the ALU (2,048
-// queries x 16 heads, 3,136 rows: 377 us, 8.7 TB/s of rows, 139 TFLOP/s).
+// queries x 16 heads, 3,136 rows: 379 us, 8.7 TB/s of rows, 139 TFLOP/s).
 //
 // A warp takes 16 tokens at a time on the M side of mma.sync m16n8k16 (keys x
 // heads, then components x heads), so 8 heads fill a tile without padding; the
@@ -194,9 +194,10 @@ constexpr int min_ctas() {
 
 // Tiles of 16 tokens of a warp's step.  Two steps are in shared memory: 8 KB of
 // rows each (4 KB of 64-byte rows).  For 128-byte rows one tile a step and the 16
-// warps an SM that then fit were slower: the long chunk above 365 us with two
-// steps in shared memory and 375 with three, against 311 (two tiles side by side
-// hide each other's latencies); 96 sequences 48.7 and 47.5 against 49.6.
+// warps an SM that then fit were slower: the long chunk above, with weights of one
+// part, 365 us with two steps in shared memory and 375 with three, against 311 (two
+// tiles side by side hide each other's latencies); 96 sequences 48.7 and 47.5
+// against 49.6.
 template <int D, typename CT>
 constexpr int tiles_per_step() { return D * sizeof(CT) <= 128 ? 2 : 1; }
 
@@ -829,8 +830,8 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     if (ctas < 1) return LSA_ERR_CUDA;
     // Few rows: a cluster of CTAs shares each, while all of them run at once and
     // every warp has a step (4 rows of 4,160 tokens, 16 heads of 128, 8-bit pages:
-    // 8.7 us with 16 CTAs a row, 10.4 with 8, 14.5 with 4, 35 with one; 128 rows of up
-    // to 1,599, 4 heads of 64, bf16: 10.7 with 2, 12.5 with one, 15.0 with 4).
+    // 9.9 us with 16 CTAs a row, 12.0 with 8, 16.7 with 4, 43 with one; 128 rows of up
+    // to 1,599, 4 heads of 64, bf16: 10.4 with 2, 12.2 with one, 12.1 with 4).
     a.cluster = 1;
     while (a.cluster < kMaxCluster && a.cluster * 2 * kWarps <= steps &&
            units <= resident<D, CT, T, NT, F32>(a.cluster * 2))
@@ -838,8 +839,8 @@ int launch(AttnArgs a, int64_t rows, cudaStream_t s) {
     // Many rows: a warp takes a whole one, which needs no merge, unless the last
     // round of warps would then run long.  In microseconds a CTA that shares a row
     // takes about 4 + steps / 4, four whole rows side by side 6 + steps (8 heads of
-    // 128, 8-bit pages; 4,096 rows of 64 tokens: 39 us shared, 21 whole; 16,384 of
-    // 512: 299 and 227; 1,024 of 2,048: 59 and 66).
+    // 128, 8-bit pages; 4,096 rows of 64 tokens: 42 us shared, 23 whole; 16,384 of
+    // 512: 346 and 272; 1,024 of 2,048: 70 and 81).
     const int64_t shared = (units + ctas - 1) / ctas * (4 + (steps + kWarps - 1) / kWarps);
     const int64_t whole = (units + kWarps * ctas - 1) / (kWarps * ctas) * (6 + steps);
     a.warps = a.cluster == 1 && whole < shared ? 1 : kWarps;

@@ -194,10 +194,11 @@ struct Unit {
 };
 
 // The unit of this CTA (blockIdx.x); false where there is none.  Up to kScanned
-// sequences every CTA looks all of them over, so that a broken cu stops all CTAs;
-// of more it looks for its own in two steps, and all CTAs together look all over
-// (a token each for 1,024 sequences: 7.6 us with all looked over by every CTA, 6.6
-// in two steps; for 4,096: 43 and 35; for 65,535: 6.8 and 0.64 ms).
+// sequences every CTA looks all of them over, so that a broken cu stops all CTAs, as
+// the call promises; of more, where that takes long, it looks for its own in two
+// steps, and all CTAs together look all over (a token each, 8 query and 1 KV heads,
+// pages of 16, 1,024 sequences: 8.9 us with all looked over by every CTA, 7.7 in two
+// steps; 4,096: 43 and 22.5; 65,535: 7.5 and 0.38 ms).
 constexpr int kScanned = 1024;
 __device__ __forceinline__ bool find_unit(const WriteArgs& a, Unit& u) {
     __shared__ int found_b, broken, part;
@@ -616,7 +617,7 @@ int launch(WriteArgs a, int64_t units, bool pages, cudaStream_t s) {
     const size_t turns = (size_t)a.most_tokens * (a.rot / 4) * sizeof(float4);
     if (!pages) {
         const int64_t want = 148 * 3;
-        // few units: their lists are split over CTAs, down to the rows that a CTA takes side by side
+        // 148 SMs.  Few units: their lists are split over CTAs, down to the rows that a CTA takes side by side
         // (8,191 fp32 tokens, 8 query and 2 KV heads, pages of 128, on this kernel: one CTA an SM
         // 27.8 us, two 23.1, three 22.9, eight 26.5)
         constexpr int ROWS = kWriteThreads / (D / 16);

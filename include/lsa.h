@@ -448,14 +448,15 @@ typedef struct {
  * holds tokens of the sequence keeps the larger of that and its scale, and what
  * it holds is rounded to the larger scale; a page written from its first slot
  * on starts afresh.  Codes are rounded to nearest even; values too large for
- * the largest scale saturate; a value that is NaN or infinite is stored as NaN.
+ * the largest scale saturate; a value that is NaN or infinite, or becomes so in
+ * its rotation, is stored as NaN.
  * LSA_BF16 pages hold the rounded values.  Slots behind the last token keep
  * what they held.
  *  - The pages that one call writes must be distinct (no two sequences append
  *    into one page).
  *  - Found on the device and latched as LSA_ERR_DEVICE: cu not ascending within
  *    [0, n] (nothing is written; of more than 1,024 sequences, tokens that cu gives
- *    to any of them may be); a negative position, a position past the page table
+ *    to any of them may be); of a sequence with tokens a negative position, a position past the page table
  *    or a page id outside [0, n_pages) (that page's tokens are skipped).
  *  - No allocation, one kernel, no state kept: capturable (the library's first
  *    call on a device belongs before a capture). */
@@ -478,8 +479,9 @@ int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, con
  * products bf16 queries are exact, fp32 ones have 22 bits next to LSA_E4M3 pages
  * and 24 next to LSA_BF16; softmax weights have 22 bits next to LSA_E4M3 pages
  * (to 2^-28 of a head's largest), whatever the scales of the pages, and next to
- * LSA_BF16 24 for fp32 results and 16 for bf16 ones.  The same inputs give the same
- * bits.  No allocation, one kernel: capturable (after a first call on the device
+ * LSA_BF16 24 for fp32 results and 16 for bf16 ones.  An infinity among the
+ * selected rows of LSA_BF16 pages may come out as NaN.  The same inputs give the
+ * same bits.  No allocation, one kernel: capturable (after a first call on the device
  * outside a capture). */
 int lsa_cache_attn(const lsa_kv_cache* cache, const void* Q, const int32_t* idx, const int32_t* cnt, int64_t nq,
                    int32_t hq, int32_t dtype, int32_t max_sel, void* O, float* lse, void* stream);
