@@ -456,8 +456,9 @@ typedef struct {
  *    into one page).
  *  - Found on the device and latched as LSA_ERR_DEVICE: cu not ascending within
  *    [0, n] (nothing is written; of more than 1,024 sequences, tokens that cu gives
- *    to any of them may be); of a sequence with tokens a negative position, a position past the page table
- *    or a page id outside [0, n_pages) (that page's tokens are skipped).
+ *    to any of them may be); of a sequence with tokens a negative position, a
+ *    position past the page table or a page id outside [0, n_pages) (that page's
+ *    tokens are skipped).
  *  - No allocation, one kernel, no state kept: capturable (the library's first
  *    call on a device belongs before a capture). */
 int lsa_cache_write(const lsa_kv_cache* cache, const void* K, const void* V, const void* Q, int64_t n,
